@@ -102,6 +102,7 @@ struct Params {
   uint32_t n_mma;     // M rounded up to 16
   uint32_t per_split; // stages per CTA
   uint32_t splits;
+  uint32_t add;       // 1: add to Y (zeroed, or what it holds), 0: overwrite
   int32_t *status;
 };
 
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2) k12_linear(const __grid_constant_
         const uint32_t t = c0 + i;
         if (t < p.M) {
           float *dst = p.y + uint64_t(t) * N + row;
-          if (p.splits > 1) atomicAdd(dst, __uint_as_float(v[i]));
+          if (p.add) atomicAdd(dst, __uint_as_float(v[i]));
           else *dst = __uint_as_float(v[i]);
         }
       }
@@ -816,8 +817,14 @@ DevInfo dev_info() {
 
 namespace wc12l {
 
-int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes, uint32_t N,
-               uint32_t K, const void *d_x, uint32_t M, float *d_y, int32_t *d_status, void *stream) {
+int device_sms() {
+  const DevInfo d = dev_info();
+  return d.attr ? d.sms : 0;
+}
+
+// the argument checks of the layer, shared with the layer with adapters
+int32_t check_linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes, uint32_t N,
+                     uint32_t K, const void *d_x, uint32_t M, const float *d_y, const int32_t *d_status) {
   auto aligned = [](const void *q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; };
   if (d_w == nullptr || d_x == nullptr || d_y == nullptr || d_status == nullptr) return WC_ERR_INVALID_ARG;
   if (!aligned(d_w, 16) || !aligned(d_x, 16) || !aligned(d_y, 4) || !aligned(d_status, 4))
@@ -833,6 +840,15 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
   if (d_plan != nullptr &&
       (!aligned(d_plan, 16) || plan_bytes < wc12p::plan_lay(N, K, 0).off_ent))  // header and starts
     return WC_ERR_INVALID_ARG;
+  return WC_OK;
+}
+
+// add: the product is added to what Y holds
+int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes, uint32_t N,
+               uint32_t K, const void *d_x, uint32_t M, float *d_y, bool add, int32_t *d_status, void *stream) {
+  const int32_t rc = check_linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, d_status);
+  if (rc != WC_OK) return rc;
+  const wc12::Lay L = wc12::lay(uint64_t(N) * K, 0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   wc12l::Params p;
   p.w = static_cast<const uint8_t *>(d_w);
@@ -884,7 +900,8 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
     if (splits < 1) splits = 1;
     p.per_split = (stages + splits - 1) / splits;
     p.splits = (stages + p.per_split - 1) / p.per_split;
-    if (p.splits > 1) wc12l::k12_zero<<<unsigned(2 * di.sms), 256, 0, s>>>(p.y, uint64_t(m) * N);
+    p.add = add || p.splits > 1;
+    if (p.splits > 1 && !add) wc12l::k12_zero<<<unsigned(2 * di.sms), 256, 0, s>>>(p.y, uint64_t(m) * N);
     dim3 grid(blocks, p.splits);
     wc12l::kernel_for(shape)<<<grid, wc12l::kThreads, smem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
@@ -897,13 +914,13 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
 extern "C" int32_t wc12_linear(const void *d_w, uint64_t w_bytes, uint32_t N, uint32_t K,
                                const void *d_x, uint32_t M, float *d_y, int32_t *d_status,
                                void *stream) {
-  return wc12l::linear(d_w, w_bytes, nullptr, 0, N, K, d_x, M, d_y, d_status, stream);
+  return wc12l::linear(d_w, w_bytes, nullptr, 0, N, K, d_x, M, d_y, false, d_status, stream);
 }
 
 extern "C" int32_t wc12_linear_planned(const void *d_w, uint64_t w_bytes, const void *d_plan,
                                        uint64_t plan_bytes, uint32_t N, uint32_t K, const void *d_x,
                                        uint32_t M, float *d_y, int32_t *d_status, void *stream) {
   if (d_plan == nullptr) return WC_ERR_INVALID_ARG;
-  return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, d_status, stream);
+  return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, false, d_status, stream);
 }
 

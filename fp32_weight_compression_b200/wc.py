@@ -7,6 +7,7 @@ CPU path: if libwc.so is missing or no CUDA device is present the calls fail.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -145,6 +146,18 @@ def load() -> ctypes.CDLL:
     L.wc12_plan.argtypes = [vp, u64, u32, u32, u64, vp, u64, vp, vp]
     L.wc12_linear_planned.restype = i32
     L.wc12_linear_planned.argtypes = [vp, u64, vp, u64, u32, u32, vp, u32, vp, vp, vp]
+    f32 = ctypes.c_float
+    L.wc12_embed.restype = i32
+    L.wc12_embed.argtypes = [vp, u64, u64, u32, vp, u32, u64, f32, vp, i32, vp, vp]
+    L.wc12_linear_adapters_work_bytes.restype = u64
+    L.wc12_linear_adapters_work_bytes.argtypes = [u32, u32]
+    L.wc12_linear_adapters.restype = i32
+    L.wc12_linear_adapters.argtypes = [vp, u64, vp, u64, u32, u32, vp, u32, vp, vp, vp, vp, u32, u32, vp, vp, u64,
+                                       vp, vp]
+    L.wc12_moe_work_bytes.restype = u64
+    L.wc12_moe_work_bytes.argtypes = [u32, u32, u32]
+    L.wc12_moe.restype = i32
+    L.wc12_moe.argtypes = [vp, u64, vp, u64, u32, u32, u32, vp, vp, u32, u32, i32, vp, i32, vp, u64, vp, vp]
     L.wc_crc32_blocks.restype = i32
     L.wc_crc32_blocks.argtypes = [vp, u64, u64, vp, vp]
     L.wc_check_coder_division.restype = i32
@@ -574,6 +587,157 @@ def split12_linear(cont: torch.Tensor, N: int, K: int, x: torch.Tensor, plan=Non
     st = int(status.item())
     if st != OK:
         raise WCError(st, "wc12_linear (device status)")
+    return y
+
+
+# The operators below check their tensors, run on the tensors' device whatever
+# the current one is, and take their outputs and workspaces from the stream
+# that they run on.  Without `status` they wait and raise, as the calls above
+# do; with a status word of the caller's (int32, zero at first, on the device)
+# they only queue work, so that they can be captured into a graph, and
+# check_status() raises later for all calls that shared the word.
+
+def check_status(status: torch.Tensor, what: str = "device status") -> None:
+    """Raise if a status word that calls were given has been set (waits for
+    the current stream); the word is left as it is."""
+    _check(int(status.item()), what)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(device: torch.device, stream):
+    """The context to launch and allocate in: the device and the stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return _NO_CONTEXT
+
+
+def _want(name: str, t, dtype, shape, device) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the container's CUDA device")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    return t
+
+
+def _container(name: str, t: torch.Tensor) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a 1-D contiguous uint8 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t
+
+
+def _status_word(status, device) -> torch.Tensor:
+    if status is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call needs a status word of the caller's")
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    return _want("status", status, torch.int32, (1,), device)
+
+
+def _output(out, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want("out", out, dtype, tuple(shape), device)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    return out
+
+
+def split12_embed(cont: torch.Tensor, V: int, K: int, ids: torch.Tensor, scale: float = 1.0,
+                  dtype=torch.bfloat16, out=None, status=None, stream=None) -> torch.Tensor:
+    """scale * table[ids] (bf16, or fp32) with the V x K bf16 table given as a
+    Split12 container on the device (wc12_embed); ids int32 or int64 of any
+    shape.  An id outside [0, V) gives a row of zeros and an error."""
+    dev = _container("cont", cont).device
+    _want("ids", ids, (torch.int64, torch.int32), None, dev)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("the output is bf16 or fp32")
+    with _on(dev, stream):
+        ids = ids.contiguous()
+        y = _output(out, (*ids.shape, K), dtype, dev)
+        st = _status_word(status, dev)
+        _check(load().wc12_embed(cont.data_ptr(), cont.numel(), V, K, ids.data_ptr(), ids.element_size(),
+                                 ids.numel(), scale, y.data_ptr(), _DT[dtype], st.data_ptr(), _stream(None)),
+               "wc12_embed")
+        if status is None:
+            check_status(st, "wc12_embed (device status)")
+    return y
+
+
+def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor, adapter: torch.Tensor,
+                            a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor, plan=None, out=None,
+                            status=None, stream=None) -> torch.Tensor:
+    """x W^T + s_a (x A_a^T) B_a^T (fp32, M x N), a = adapter[m] (int32, -1 for
+    none), with W (N x K bf16) given as a Split12 container on the device
+    (wc12_linear_adapters): x M x K bf16, a L x r x K and b L x N x r bf16,
+    scales L fp32.  The plan serves batches of more than 16 tokens."""
+    dev = _container("cont", cont).device
+    if x.dim() != 2 or a.dim() != 3:
+        raise ValueError("x must be M x K and a L x r x K")
+    M, (L, r, _k) = x.shape[0], a.shape
+    _want("x", x, torch.bfloat16, (M, K), dev)
+    _want("adapter", adapter, torch.int32, (M,), dev)
+    _want("a", a, torch.bfloat16, (L, r, K), dev)
+    _want("b", b, torch.bfloat16, (L, N, r), dev)
+    _want("scales", scales, torch.float32, (L,), dev)
+    if plan is not None:
+        _container("plan", plan)
+        _want("plan", plan, torch.uint8, None, dev)
+    lib = load()
+    with _on(dev, stream):
+        x, adapter, a, b, scales = (t.contiguous() for t in (x, adapter, a, b, scales))
+        y = _output(out, (M, N), torch.float32, dev)
+        st = _status_word(status, dev)
+        work = torch.empty(M * r, dtype=torch.float32, device=dev)
+        _check(lib.wc12_linear_adapters(cont.data_ptr(), cont.numel(), None if plan is None else plan.data_ptr(),
+                                        0 if plan is None else plan.numel(), N, K, x.data_ptr(), M,
+                                        adapter.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), L, r,
+                                        y.data_ptr(), work.data_ptr(), 4 * work.numel(), st.data_ptr(),
+                                        _stream(None)), "wc12_linear_adapters")
+        if status is None:
+            check_status(st, "wc12_linear_adapters (device status)")
+    return y
+
+
+def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: int, x: torch.Tensor,
+                logits: torch.Tensor, k: int, renormalize: bool = True, dtype=torch.bfloat16, out=None,
+                status=None, stream=None) -> torch.Tensor:
+    """A mixture-of-experts layer for a few tokens (T x H, bf16 or fp32), from
+    the router's logits (T x E fp32) on, with the experts' weights given as
+    two Split12 containers on the device, gate_up E x 2F x H and down
+    E x H x F (wc12_moe): the k experts with the largest logits, their softmax
+    (over themselves, or without renormalize over all experts), SiLU-gated."""
+    dev = _container("gate_up", gate_up).device
+    _container("down", down)
+    _want("down", down, torch.uint8, None, dev)
+    if x.dim() != 2:
+        raise ValueError("x must be T x H")
+    T = x.shape[0]
+    _want("x", x, torch.bfloat16, (T, H), dev)
+    _want("logits", logits, torch.float32, (T, E), dev)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("the output is bf16 or fp32")
+    lib = load()
+    with _on(dev, stream):
+        x, logits = x.contiguous(), logits.contiguous()
+        y = _output(out, (T, H), dtype, dev)
+        st = _status_word(status, dev)
+        work = torch.empty(lib.wc12_moe_work_bytes(T, k, F), dtype=torch.uint8, device=dev)
+        _check(lib.wc12_moe(gate_up.data_ptr(), gate_up.numel(), down.data_ptr(), down.numel(), E, H, F,
+                            x.data_ptr(), logits.data_ptr(), T, k, 1 if renormalize else 0, y.data_ptr(),
+                            _DT[dtype], work.data_ptr(), work.numel(), st.data_ptr(), _stream(None)),
+               "wc12_moe")
+        if status is None:
+            check_status(st, "wc12_moe (device status)")
     return y
 
 

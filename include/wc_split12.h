@@ -161,6 +161,83 @@ WC_API int32_t wc12_linear_planned(const void *d_w, uint64_t w_bytes, const void
                                    uint64_t plan_bytes, uint32_t N, uint32_t K, const void *d_x,
                                    uint32_t M, float *d_y, int32_t *d_status, void *stream);
 
+/* Embedding lookup out of a table held as a Split12 container, only the rows
+ * asked for read: out[t, :] = scale * table[ids[t], :].
+ *   d_w, w_bytes  the container (16-byte aligned; as for wc12_linear), n = V * K
+ *   V, K          rows of the table; K a multiple of 8
+ *   d_ids         T row numbers, id_bytes 4 (int32) or 8 (int64) each, aligned
+ *                 to their size, in any order, repeated or not
+ *   scale         multiplied in fp32; with 1 a bf16 output has the table's bits
+ *   d_out         T x K, 16-byte aligned; out_dtype WC_BF16 (rounded once, to
+ *                 nearest) or WC_FP32
+ *   d_status      device i32 set to 0 by the caller: WC_ERR_CORRUPT for a bad
+ *                 container, WC_ERR_INVALID_ARG for an id outside [0, V), whose
+ *                 row is set to zeros
+ * T = 0 does nothing.  One launch.  Returns WC_OK, WC_ERR_INVALID_ARG or
+ * WC_ERR_CUDA. */
+WC_API int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uint32_t K,
+                          const void *d_ids, uint32_t id_bytes, uint64_t T, float scale,
+                          void *d_out, int32_t out_dtype, int32_t *d_status, void *stream);
+
+/* The linear layer with low-rank adapters of many requests beside it:
+ *   y[m] = x[m] W^T + s_a (x[m] A_a^T) B_a^T,  a = adapter[m]
+ * with W as for wc12_linear, its plan (d_plan, plan_bytes) or NULL, 0 (the
+ * plan serves batches of more than 16 tokens), and
+ *   d_adapter     M int32: a token's adapter, 0 .. L - 1, or -1 for none
+ *   d_a, d_b      L x r x K and L x N x r bf16, row-major, 16-byte aligned
+ *   d_scale       L fp32
+ *   L, r          adapters; the rank, a multiple of 8 up to 256 (a smaller
+ *                 one is padded with zero rows of A and zero columns of B)
+ *   d_y           M x N fp32, row-major (overwritten)
+ *   d_work        wc12_linear_adapters_work_bytes(M, r) bytes, 16-byte
+ *                 aligned, for this call alone until it is done
+ *   d_status      as for wc12_linear; WC_ERR_INVALID_ARG for an adapter
+ *                 outside [-1, L), whose token gets the shared product only
+ * K at most 2^20.  Up to 16 tokens the result is the same bits every time;
+ * beyond, as for wc12_linear, sums of parts of K are added in any order.
+ * Two launches up to 16 tokens, then three and more (a token slice each).
+ * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY (work_bytes too small)
+ * or WC_ERR_CUDA. */
+WC_API uint64_t wc12_linear_adapters_work_bytes(uint32_t M, uint32_t r);
+WC_API int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const void *d_plan,
+                                    uint64_t plan_bytes, uint32_t N, uint32_t K, const void *d_x,
+                                    uint32_t M, const int32_t *d_adapter, const void *d_a,
+                                    const void *d_b, const float *d_scale, uint32_t L, uint32_t r,
+                                    float *d_y, void *d_work, uint64_t work_bytes,
+                                    int32_t *d_status, void *stream);
+
+/* A mixture-of-experts layer for a few tokens, from the router's logits on:
+ *   S_t    = the k experts with the largest logits of token t (equal logits:
+ *            the lower expert; an expert with logit -inf is never chosen)
+ *   p      = softmax of the logits over S_t (renormalize != 0) or over all E
+ *   out[t] = sum over e in S_t of p_e D_e (silu(G_e x_t) * (U_e x_t))
+ * Only the chosen experts' weights are read.
+ *   d_gate_up     Split12 container of E x 2F x H values: expert e's rows are
+ *                 the F rows of G_e, then the F rows of U_e
+ *   d_down        Split12 container of E x H x F values: D_e
+ *                 (each 16-byte aligned, its buffer's size with it)
+ *   E, H, F, k    1 <= k <= E <= 512, k <= 16; H and F multiples of 64, at most
+ *                 2^20; chosen experts (at most 32 k) times ceil(F / 128) at
+ *                 most 65536
+ *   d_x           T x H bf16, 16-byte aligned; d_logits T x E fp32
+ *   d_out         T x H, WC_BF16 (rounded once) or WC_FP32 (the gated values
+ *                 enter the down product with 16 bits: off by 2^-18 of each)
+ *   d_work        wc12_moe_work_bytes(T, k, F) bytes, 16-byte aligned, for this
+ *                 call alone until it is done
+ *   d_status      device i32 set to 0 by the caller: WC_ERR_CORRUPT for a bad
+ *                 container
+ * A token whose logits are all -inf gets zeros; one with a NaN or +inf among
+ * them a row of NaN.  A token's row does not depend on the other tokens'
+ * values.  Two launches for each 32 tokens; the same bits every time.  T = 0
+ * does nothing.  Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
+ * (work_bytes too small) or WC_ERR_CUDA. */
+WC_API uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F);
+WC_API int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const void *d_down,
+                        uint64_t down_bytes, uint32_t E, uint32_t H, uint32_t F, const void *d_x,
+                        const float *d_logits, uint32_t T, uint32_t k, int32_t renormalize,
+                        void *d_out, int32_t out_dtype, void *d_work, uint64_t work_bytes,
+                        int32_t *d_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
