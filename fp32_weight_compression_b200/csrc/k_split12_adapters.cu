@@ -60,15 +60,16 @@ __device__ __forceinline__ void split3(float v, uint32_t &h0, uint32_t &h1, uint
 }
 
 // ---------------------------------------------------------------------------
-// t[m][j] = s_a sum_k x[m][k] A_a[j][k].  A CTA takes 8 tokens (blockIdx.x),
-// 16 ranks (y) and one adapter: that of token z of the 8, if it is the first
-// with it.  Its 8 warps split K, 64 values at a time (16 a lane, as in
-// wc12_few.cuh, A's rows in the place of the weights').
-__global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_constant__ Params p) {
+// t[m][j] = s_a sum_k x[m][k] A_a[j][k].  A cluster takes 8 tokens (x), 16
+// ranks (y) and one adapter: that of token z of the 8, if it is the first
+// with it.  The warps of its CTAs split K, 64 values at a time (16 a lane, as
+// in wc12_few.cuh, A's rows in the place of the weights').
+__global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_constant__ Params p, uint32_t csize) {
   launch_dependents();
   __shared__ float red[kWarps][8 * kRedTok];
+  __shared__ float part[128];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t m0 = 8 * blockIdx.x, j0 = 16 * blockIdx.y, z = blockIdx.z;
+  const uint32_t rank = blockIdx.x % csize, m0 = 8 * (blockIdx.x / csize), j0 = 16 * blockIdx.y, z = blockIdx.z;
   int32_t ad = -1;
   if (lane < 8 && m0 + lane < p.M) ad = p.adapter[m0 + lane];
   if (ad < -1 || ad >= int32_t(p.L)) {
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
   }
   const int32_t mine = __shfl_sync(0xffffffffu, ad, z);
   const uint32_t same = __ballot_sync(0xffffffffu, lane < 8 && ad == mine);
-  if (mine < 0 || (same & ((1u << z) - 1u)) != 0) return;
+  if (mine < 0 || (same & ((1u << z) - 1u)) != 0) return;  // the whole cluster
   const bool live = (same >> g) & 1u;
   const uint16_t *px = p.x + uint64_t(m0 + g) * p.K + 16 * t;
   const bool r0 = j0 + g < p.r, r1 = j0 + g + 8 < p.r;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
   float tot[1][4] = {};
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 4
-  for (uint32_t k = 64 * warp; k < p.K; k += 64 * kWarps) {
+  for (uint32_t k = 64 * (rank * kWarps + warp); k < p.K; k += 64 * kWarps * csize) {
     uint4 a0[2] = {zero, zero}, a1[2] = {zero, zero}, xv[2] = {zero, zero};
     if (r0) {
       a0[0] = *reinterpret_cast<const uint4 *>(pa + k);
@@ -111,118 +112,137 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
   }
   put_sums<1>(red[warp], tot, lane);
   __syncthreads();
-  if (tid < 128) {
-    const uint32_t j = tid & 15, m = tid >> 4;
-    float sum = 0.0f;
+  const uint32_t j = tid & 15, m = tid >> 4;
+  float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) sum += red[w][m * kRedTok + j];
-    if (((same >> m) & 1u) && j0 + j < p.r) p.t[uint64_t(m0 + m) * p.r + j0 + j] = p.scale[mine] * sum;
+  for (int w = 0; w < kWarps; w++) sum += red[w][m * kRedTok + j];
+  if (csize > 1) {
+    part[tid] = sum;
+    cluster_sync();
+    if (rank == 0) {
+      sum = 0.0f;
+      for (uint32_t c = 0; c < csize; c++) sum += cluster_load(&part[tid], c);
+    }
+    cluster_sync();  // the others' sums are read until here
   }
+  if (rank == 0 && ((same >> m) & 1u) && j0 + j < p.r) p.t[uint64_t(m0 + m) * p.r + j0 + j] = p.scale[mine] * sum;
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: 16 weight rows a cluster (its CTAs split K), all tokens.
-struct FewSmem {
-  Lists lists;
-  float part[kFewTokens * kRows];  // the CTA's sums, [token][row]
+// Few tokens: a CTA takes 64 weight rows, 16 a warp, and all tokens; the CTAs
+// of a cluster split K.
+template <int NT>
+struct Few {
+  using R = Ring<1, NT, 1>;
+  static constexpr uint32_t kDepth = NT == 1 ? 4 : 3;
+  static constexpr uint32_t kSums = 8 * NT * kRedTok;  // floats a warp
+  static constexpr uint32_t kLists = kWarps * kDepth * R::kBytes;
+  static constexpr uint32_t kRed = kLists + kWarps * kListCap * 4;
+  static constexpr uint32_t kSmem = kRed + kWarps * kSums * 4;
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) k12_few_adapters(const __grid_constant__ Params p, uint32_t csize) {
-  __shared__ FewSmem s;
+__global__ void __launch_bounds__(kThreads) k12_few_adapters(const __grid_constant__ Params p, uint32_t csize) {
+  using F = Few<NT>;
+  extern __shared__ __align__(16) uint8_t dyn[];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kRows;
-  const uint32_t K = p.K, stages = (K + kStage - 1) / kStage, step = kWarps * csize;
+  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * (kRows * kWarps), row0 = n0 + kRows * warp;
+  const uint32_t K = p.K, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
   View v;
   open_planes(v, p.w, uint64_t(p.N) * K);
-  // stage it of this warp is stage gw + it * step of the row
-  const uint32_t gw = rank * kWarps + warp;
-  const uint8_t *pi = v.idx + (uint64_t(n0 + g) * K) / 2 + 8 * t, *pl = v.lo + uint64_t(n0 + g) * K + 16 * t;
-  const uint32_t its = gw < stages ? (stages - gw + step - 1) / step : 0u;
-  auto k_of = [&](uint32_t it) { return (gw + it * step) * kStage; };
-  Frag f[2];
-#pragma unroll
-  for (uint32_t i = 0; i < 2; i++)
-    if (i < its) load_frag(f[i], pi + k_of(i) / 2, pl + k_of(i), K, k_of(i) + 64 < K);
-  const bool ok = open_header(v, p.w, p.w_bytes);  // the same in every CTA
-  if (!ok) {
-    if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
-    wait_prerequisites();
-    return;
-  }
-  gather(s.lists, v, K, 1, [&](uint32_t) { return uint64_t(n0); },
-         [&](uint32_t, uint32_t stage, uint32_t &w, uint32_t &it) {
-           const uint32_t o = stage % step;
-           w = o % kWarps;
-           it = stage / step;
-           return o / kWarps == rank;
-         },
-         p.status);
-  const Exceptions x = exceptions_of(s.lists, warp, lane, (stages + step - 1) / step);
+  Window win;
+  window_offsets(win, v.exc_off, row0, K, lane);
+  const uint64_t row_g = row0 + g, at = row_g * K + u0 * kUnit;
+  const uint8_t *pi = v.idx + at / 2 + 8 * t, *pl = v.lo + at + 16 * t;
   const uint16_t *px[NT];
-  uint32_t live = 0;
+  uint32_t live = 0, tiles = 0;
 #pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    const uint32_t m = 8 * nt + g;
-    live |= m < p.M ? 1u << nt : 0u;
-    px[nt] = p.x + uint64_t(m) * K + 16 * t;
+  for (int i = 0; i < NT; i++) {
+    const uint32_t m = 8 * i + g;
+    live |= m < p.M ? 1u << i : 0u;
+    tiles |= 8u * i < p.M ? 1u << i : 0u;
+    px[i] = p.x + uint64_t(m < p.M ? m : 0u) * K + u0 * kUnit + 16 * t;
   }
-  float tot[NT][4] = {};
-  for (uint32_t it0 = 0; it0 < its; it0 += 2) {
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * F::kDepth * F::R::kBytes;
+  auto load = [&](uint32_t u, uint32_t slot) {  // u from u0
+    if (u < u1) {
+      F::R::load(ring + slot * F::R::kBytes, lane, &pi, &pl, K, px, live, tiles, 0);
+      pi += kUnit / 2;
+      pl += kUnit;
 #pragma unroll
-    for (uint32_t i = 0; i < 2; i++) {
-      const uint32_t it = it0 + i;
-      if (it >= its) break;
-      const uint32_t k0 = k_of(it);
-      const uint16_t *q[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) q[nt] = px[nt] + k0;
-      const bool second = k0 + 64 < K;
-      if (x.walk) stage_product<NT, 1, false, true>(tot, f[i], v, q, live, ~0u, 0, second, x, it, n0 + g, K, k0, lane);
-      else stage_product<NT, 1, false, false>(tot, f[i], v, q, live, ~0u, 0, second, x, it, n0 + g, K, k0, lane);
-      if (it + 2 < its) {
-        const uint32_t k2 = k_of(it + 2);
-        load_frag(f[i], pi + k2 / 2, pl + k2, K, k2 + 64 < K);
-      }
+      for (int i = 0; i < NT; i++) px[i] += kUnit;
     }
-  }
-  __syncthreads();  // the lists are read until here
-  put_sums<NT>(s.lists.sums(warp, NT), tot, lane);
-  __syncthreads();
-  constexpr uint32_t kOut = 8 * NT * kRows;
-  for (uint32_t o = tid; o < kOut; o += kThreads) {
-    const uint32_t row = o % kRows, m = o / kRows;
-    float sum = 0.0f;
+    copies_commit();
+  };
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) sum += s.lists.sums(w, NT)[m * kRedTok + row];
-    s.part[o] = sum;
+  for (uint32_t i = 0; i < F::kDepth; i++) load(u0 + i, i);
+  Exceptions x;
+  x.list = reinterpret_cast<uint32_t *>(dyn + F::kLists) + warp * kListCap;
+  exceptions_reset(x);
+  const bool ok = open_header(v, p.w, p.w_bytes);  // the same in every CTA
+  float tot[1][NT][4] = {};
+  if (ok) {
+    if (v.ne > 0) {
+      window_entries(win, v, lane);
+      window_keep(x, win, v, row0, K, 0, u0, u1, lane, p.status);
+      exceptions_ready(x, lane);
+    }
+    uint32_t slot = 0;
+    for (uint32_t u = u0; u < u1; u++) {
+      copies_wait<F::kDepth - 1>();
+      unit_product<1, NT, 1>(tot, ring + slot * F::R::kBytes, v.book, v, tiles, x, u, &row_g, K, lane);
+      load(u + F::kDepth, slot);
+      slot = slot + 1 == F::kDepth ? 0 : slot + 1;
+    }
+  } else if (blockIdx.x == 0 && tid == 0) {
+    report(p.status, WC_ERR_CORRUPT);
   }
+  copies_wait<0>();
+  float *red = reinterpret_cast<float *>(dyn + F::kRed);
+  put_sums<NT>(red + warp * F::kSums, tot[0], lane);
   if (csize > 1) cluster_sync(); else __syncthreads();
   wait_prerequisites();  // t
-  for (uint32_t o = tid + rank * kThreads; o < kOut; o += kThreads * csize) {
-    const uint32_t row = o % kRows, m = o / kRows;
-    if (m >= p.M) continue;
-    float sum = s.part[o];
-    if (csize > 1) {
-      sum = 0.0f;
-      for (uint32_t c = 0; c < csize; c++) sum += cluster_load(&s.part[o], c);
-    }
-    const int32_t ad = p.adapter[m];
-    if (ad >= 0 && ad < int32_t(p.L)) {
-      const uint4 *pb = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad) * p.N + n0 + row) * p.r);
-      const float4 *pt = reinterpret_cast<const float4 *>(p.t + uint64_t(m) * p.r);
-      float add = 0.0f;
-      for (uint32_t j = 0; j < p.r / 8; j++) {
-        const uint4 b = pb[j];
-        const float4 t0 = pt[2 * j], t1 = pt[2 * j + 1];
-        add += t0.x * bf16_lo(b.x) + t0.y * bf16_hi(b.x) + t0.z * bf16_lo(b.y) + t0.w * bf16_hi(b.y);
-        add += t1.x * bf16_lo(b.z) + t1.y * bf16_hi(b.z) + t1.z * bf16_lo(b.w) + t1.w * bf16_hi(b.w);
+  if (ok) {
+    constexpr uint32_t kOutRows = kRows * kWarps;
+    for (uint32_t o = tid + rank * kThreads; o < 8 * NT * kOutRows; o += kThreads * csize) {
+      const uint32_t row = o % kOutRows, m = o / kOutRows;
+      if (m >= p.M) break;
+      const float *from = red + row / kRows * F::kSums + m * kRedTok + row % kRows;
+      float sum = 0.0f;
+      if (csize > 1)
+        for (uint32_t c = 0; c < csize; c++) sum += cluster_load(from, c);
+      else
+        sum = *from;
+      const int32_t ad = p.adapter[m];
+      if (ad >= 0 && ad < int32_t(p.L)) {
+        const uint4 *pb = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad) * p.N + n0 + row) * p.r);
+        const float4 *pt = reinterpret_cast<const float4 *>(p.t + uint64_t(m) * p.r);
+        float add = 0.0f;
+        for (uint32_t j = 0; j < p.r / 8; j++) {
+          const uint4 b = pb[j];
+          const float4 t0 = pt[2 * j], t1 = pt[2 * j + 1];
+          add += t0.x * bf16_lo(b.x) + t0.y * bf16_hi(b.x) + t0.z * bf16_lo(b.y) + t0.w * bf16_hi(b.y);
+          add += t1.x * bf16_lo(b.z) + t1.y * bf16_hi(b.z) + t1.z * bf16_lo(b.w) + t1.w * bf16_hi(b.w);
+        }
+        sum += add;
       }
-      sum += add;
+      p.y[uint64_t(m) * p.N + n0 + row] = sum;
     }
-    p.y[uint64_t(m) * p.N + n0 + row] = sum;
   }
   if (csize > 1) cluster_sync();  // the others' sums are read until here
+}
+
+template <int NT>
+cudaError_t launch_few(const Params &p, int sms, cudaStream_t s) {
+  using F = Few<NT>;
+  if (cudaFuncSetAttribute(k12_few_adapters<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::kSmem)) != cudaSuccess)
+    return cudaGetLastError();
+  // CTAs that split K: as many as run at once (4 an SM), while each keeps
+  // a ring's worth of units
+  const uint32_t blocks = p.N / (kRows * kWarps), units = p.K / kUnit;
+  uint32_t csize = 1;
+  while (csize < 8 && blocks * csize * 2 <= 4u * uint32_t(sms) && units >= 2 * csize * F::kDepth) csize *= 2;
+  return launch(k12_few_adapters<NT>, dim3(blocks * csize), csize, F::kSmem, s, true, p, csize);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +321,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
     return WC_ERR_INVALID_ARG;
   if (!aligned(d_adapter, 4) || !aligned(d_a, 16) || !aligned(d_b, 16) || !aligned(d_scale, 4) || !aligned(d_work, 16))
     return WC_ERR_INVALID_ARG;
-  if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > (1u << 20) || N / 128 > 65535 || M > 0x7FFFFFFFu)
+  if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > kMaxK || N / (kRows * kWarps) > 65535 || M > 0x7FFFFFFFu)
     return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_linear_adapters_work_bytes(M, r)) return WC_ERR_CAPACITY;
   const int sms = wc12l::device_sms();
@@ -323,18 +343,15 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   p.L = L;
   p.status = d_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  k12_adapter_shrink<<<dim3((M + 7) / 8, (r + 15) / 16, M < 8 ? M : 8), kThreads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
-  if (M <= kFewTokens) {
-    // CTAs that split K: until every SM has two, while each warp has a stage
-    const uint32_t groups = N / kRows, stages = (K + kStage - 1) / kStage;
-    uint32_t csize = 1;
-    while (csize < 8 && groups * csize < 2u * uint32_t(sms) && stages >= 2 * csize * kWarps) csize *= 2;
-    auto kernel = M <= 8 ? k12_few_adapters<1> : k12_few_adapters<2>;
-    if (launch(kernel, dim3(groups * csize), csize, s, true, p, csize) != cudaSuccess) return WC_ERR_CUDA;
-    return WC_OK;
+  {
+    const uint32_t tiles = (M + 7) / 8, ranks = (r + 15) / 16, z = M < 8 ? M : 8;
+    uint32_t csize = 1;  // CTAs that split K: until each SM has two, while a warp has two pieces
+    while (csize < 8 && tiles * ranks * csize < 2u * uint32_t(sms) && K / 64 >= 4 * csize * kWarps) csize *= 2;
+    if (launch(k12_adapter_shrink, dim3(tiles * csize, ranks, z), csize, 0, s, false, p, csize) != cudaSuccess)
+      return WC_ERR_CUDA;
   }
-  if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kWarps)), 1, s, true, p) != cudaSuccess)
+  if (M <= kFewTokens) return (M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s)) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
+  if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kWarps)), 1, 0, s, true, p) != cudaSuccess)
     return WC_ERR_CUDA;
   return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, true, d_status, stream);
 }

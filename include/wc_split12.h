@@ -193,7 +193,7 @@ WC_API int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uint32_
  *                 aligned, for this call alone until it is done
  *   d_status      as for wc12_linear; WC_ERR_INVALID_ARG for an adapter
  *                 outside [-1, L), whose token gets the shared product only
- * K at most 2^20.  Up to 16 tokens the result is the same bits every time;
+ * K at most 65536, N at most 2^22 - 64.  Up to 16 tokens the result is the same bits every time;
  * beyond, as for wc12_linear, sums of parts of K are added in any order.
  * Two launches up to 16 tokens, then three and more (a token slice each).
  * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY (work_bytes too small)
@@ -217,8 +217,7 @@ WC_API int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const voi
  *   d_down        Split12 container of E x H x F values: D_e
  *                 (each 16-byte aligned, its buffer's size with it)
  *   E, H, F, k    1 <= k <= E <= 512, k <= 16; H and F multiples of 64, at most
- *                 2^20; chosen experts (at most 32 k) times ceil(F / 128) at
- *                 most 65536
+ *                 65536
  *   d_x           T x H bf16, 16-byte aligned; d_logits T x E fp32
  *   d_out         T x H, WC_BF16 (rounded once) or WC_FP32 (the gated values
  *                 enter the down product with 16 bits: off by 2^-18 of each)
