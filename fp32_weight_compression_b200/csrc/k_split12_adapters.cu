@@ -24,7 +24,6 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
                const void *d_x, uint32_t M, float *d_y, bool add, int32_t *d_status, void *stream);
 int32_t check_linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes, uint32_t N, uint32_t K,
                      const void *d_x, uint32_t M, const float *d_y, const int32_t *d_status);
-int device_sms();
 }  // namespace wc12l
 
 namespace wc12a {
@@ -33,6 +32,8 @@ using namespace wc12f;
 
 constexpr uint32_t kFewTokens = 16;
 constexpr uint32_t kMaxRank = 256;
+// of the two small products with A and B
+constexpr int kSideWarps = 4, kSideThreads = 32 * kSideWarps;
 
 struct Params {
   const uint8_t *w;
@@ -64,9 +65,9 @@ __device__ __forceinline__ void split3(float v, uint32_t &h0, uint32_t &h1, uint
 // ranks (y) and one adapter: that of token z of the 8, if it is the first
 // with it.  The warps of its CTAs split K, 64 values at a time (16 a lane, as
 // in wc12_few.cuh, A's rows in the place of the weights').
-__global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_constant__ Params p, uint32_t csize) {
+__global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_constant__ Params p, uint32_t csize) {
   launch_dependents();
-  __shared__ float red[kWarps][8 * kRedTok];
+  __shared__ float red[kSideWarps][8 * kRedTok];
   __shared__ float part[128];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t rank = blockIdx.x % csize, m0 = 8 * (blockIdx.x / csize), j0 = 16 * blockIdx.y, z = blockIdx.z;
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
   float tot[1][4] = {};
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 4
-  for (uint32_t k = 64 * (rank * kWarps + warp); k < p.K; k += 64 * kWarps * csize) {
+  for (uint32_t k = 64 * (rank * kSideWarps + warp); k < p.K; k += 64 * kSideWarps * csize) {
     uint4 a0[2] = {zero, zero}, a1[2] = {zero, zero}, xv[2] = {zero, zero};
     if (r0) {
       a0[0] = *reinterpret_cast<const uint4 *>(pa + k);
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
   const uint32_t j = tid & 15, m = tid >> 4;
   float sum = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) sum += red[w][m * kRedTok + j];
+  for (int w = 0; w < kSideWarps; w++) sum += red[w][m * kRedTok + j];
   if (csize > 1) {
     part[tid] = sum;
     cluster_sync();
@@ -129,90 +130,95 @@ __global__ void __launch_bounds__(kThreads) k12_adapter_shrink(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: a CTA takes 64 weight rows, 16 a warp, and all tokens; the CTAs
-// of a cluster split K.
+// Few tokens: a CTA takes 64 weight rows and all tokens, the CTAs of a
+// cluster split K.  A stage's two subtiles are successive ranges of K.
 template <int NT>
 struct Few {
-  using R = Ring<1, NT, 1>;
-  static constexpr uint32_t kDepth = NT == 1 ? 4 : 3;
-  static constexpr uint32_t kSums = 8 * NT * kRedTok;  // floats a warp
-  static constexpr uint32_t kLists = kWarps * kDepth * R::kBytes;
-  static constexpr uint32_t kRed = kLists + kWarps * kListCap * 4;
-  static constexpr uint32_t kSmem = kRed + kWarps * kSums * 4;
+  static constexpr uint32_t kStage = stage_bytes(8 * NT);
+  static constexpr uint32_t kOwn = own_words(8 * NT);  // a warp's list, then its sums
+  static constexpr uint32_t kLists = kDepth * kStage;
+  static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
+  static constexpr uint32_t kSmem = kBars + sizeof(Bars);
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads) k12_few_adapters(const __grid_constant__ Params p, uint32_t csize) {
+__global__ void __launch_bounds__(kThreads, 3) k12_few_adapters(const __grid_constant__ Params p,
+                                                                const __grid_constant__ Planes planes, uint32_t csize) {
   using F = Few<NT>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * (kRows * kWarps), row0 = n0 + kRows * warp;
+  extern __shared__ __align__(128) uint8_t dyn[];
+  Bars &bars = *reinterpret_cast<Bars *>(dyn + F::kBars);
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kSubRows;
   const uint32_t K = p.K, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
+  const uint32_t stages = (u1 - u0 + 1) / 2, ring = smem_u32(dyn);
   View v;
   open_planes(v, p.w, uint64_t(p.N) * K);
-  Window win;
-  window_offsets(win, v.exc_off, row0, K, lane);
-  const uint64_t row_g = row0 + g, at = row_g * K + u0 * kUnit;
-  const uint8_t *pi = v.idx + at / 2 + 8 * t, *pl = v.lo + at + 16 * t;
-  const uint16_t *px[NT];
-  uint32_t live = 0, tiles = 0;
-#pragma unroll
-  for (int i = 0; i < NT; i++) {
-    const uint32_t m = 8 * i + g;
-    live |= m < p.M ? 1u << i : 0u;
-    tiles |= 8u * i < p.M ? 1u << i : 0u;
-    px[i] = p.x + uint64_t(m < p.M ? m : 0u) * K + u0 * kUnit + 16 * t;
+  if (tid == 0) bars_init(bars);
+  __syncthreads();
+  bool ok;
+  float *red = reinterpret_cast<float *>(dyn + F::kLists);
+  if (warp == kWarps) {
+    auto load = [&](uint32_t s) {
+      uint64_t *full = &bars.full[s % kDepth];
+      const uint32_t slot = ring + s % kDepth * F::kStage, u = u0 + 2 * s, subs = u + 1 < u1 ? 2 : 1;
+      if (lane == 0) {
+        bar_expect(full, subs * (kSubBytes + p.M * 2 * kUnit));
+        for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (u + i) * kUnit, n0, full);
+      }
+      __syncwarp();
+      if (lane < p.M) load_row(slot + 2 * kSubBytes + lane * kXRow, p.x + uint64_t(lane) * K + u * kUnit, subs * 2 * kUnit, full);
+    };
+    uint32_t s = 0;
+    for (; s < kDepth && s < stages; s++) load(s);
+    ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
+    for (; ok && s < stages; s++) {
+      if (!bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) break;
+      load(s);
+    }
+    // no copy is in flight when the CTA ends
+    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+  } else {
+    const uint32_t group = warp & 3, sub = warp >> 2, row0 = n0 + kRows * group;
+    Window win;
+    window_offsets(win, v.exc_off, row0, K, lane);
+    Exceptions x;
+    x.list = reinterpret_cast<uint32_t *>(dyn + F::kLists) + warp * F::kOwn;
+    exceptions_reset(x);
+    ok = open_header(v, p.w, p.w_bytes);
+    float tot[NT][4] = {};
+    if (ok) {
+      if (v.ne > 0) {
+        window_entries(win, v, lane);
+        window_keep(x, win, v, row0, K, u0 + sub, u1, 2, lane, p.status);
+        exceptions_ready(x, lane);
+      }
+      for (uint32_t s = 0; s < stages; s++) {
+        if (!bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status)) break;
+        const uint32_t slot = ring + s % kDepth * F::kStage, at = slot + sub * kSubBytes, u = u0 + 2 * s + sub;
+        if (u < u1)
+          unit_product<NT, 1>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64,
+                              slot + 2 * kSubBytes + sub * 2 * kUnit, v.book, v, x, u, row0 + (lane >> 2), K, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
+      }
+    } else if (blockIdx.x == 0 && tid == 0) {
+      report(p.status, WC_ERR_CORRUPT);
+    }
+    __syncwarp();
+    put_sums<NT>(red + warp * F::kOwn, tot, lane);
   }
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * F::kDepth * F::R::kBytes;
-  auto load = [&](uint32_t u, uint32_t slot) {  // u from u0
-    if (u < u1) {
-      F::R::load(ring + slot * F::R::kBytes, lane, &pi, &pl, K, px, live, tiles, 0);
-      pi += kUnit / 2;
-      pl += kUnit;
-#pragma unroll
-      for (int i = 0; i < NT; i++) px[i] += kUnit;
-    }
-    copies_commit();
-  };
-#pragma unroll
-  for (uint32_t i = 0; i < F::kDepth; i++) load(u0 + i, i);
-  Exceptions x;
-  x.list = reinterpret_cast<uint32_t *>(dyn + F::kLists) + warp * kListCap;
-  exceptions_reset(x);
-  const bool ok = open_header(v, p.w, p.w_bytes);  // the same in every CTA
-  float tot[1][NT][4] = {};
-  if (ok) {
-    if (v.ne > 0) {
-      window_entries(win, v, lane);
-      window_keep(x, win, v, row0, K, 0, u0, u1, lane, p.status);
-      exceptions_ready(x, lane);
-    }
-    uint32_t slot = 0;
-    for (uint32_t u = u0; u < u1; u++) {
-      copies_wait<F::kDepth - 1>();
-      unit_product<1, NT, 1>(tot, ring + slot * F::R::kBytes, v.book, v, tiles, x, u, &row_g, K, lane);
-      load(u + F::kDepth, slot);
-      slot = slot + 1 == F::kDepth ? 0 : slot + 1;
-    }
-  } else if (blockIdx.x == 0 && tid == 0) {
-    report(p.status, WC_ERR_CORRUPT);
-  }
-  copies_wait<0>();
-  float *red = reinterpret_cast<float *>(dyn + F::kRed);
-  put_sums<NT>(red + warp * F::kSums, tot[0], lane);
   if (csize > 1) cluster_sync(); else __syncthreads();
   wait_prerequisites();  // t
   if (ok) {
-    constexpr uint32_t kOutRows = kRows * kWarps;
-    for (uint32_t o = tid + rank * kThreads; o < 8 * NT * kOutRows; o += kThreads * csize) {
-      const uint32_t row = o % kOutRows, m = o / kOutRows;
+    for (uint32_t o = tid + rank * kThreads; o < 8 * NT * kSubRows; o += kThreads * csize) {
+      const uint32_t row = o % kSubRows, m = o / kSubRows;
       if (m >= p.M) break;
-      const float *from = red + row / kRows * F::kSums + m * kRedTok + row % kRows;
+      const float *from = red + row / kRows * F::kOwn + m * kRedTok + row % kRows;
       float sum = 0.0f;
-      if (csize > 1)
-        for (uint32_t c = 0; c < csize; c++) sum += cluster_load(from, c);
-      else
-        sum = *from;
+      for (uint32_t c = 0; c < csize; c++) {
+        if (csize > 1) sum += cluster_load(from, c) + cluster_load(from + 4 * F::kOwn, c);
+        else sum = from[0] + from[4 * F::kOwn];
+      }
       const int32_t ad = p.adapter[m];
       if (ad >= 0 && ad < int32_t(p.L)) {
         const uint4 *pb = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad) * p.N + n0 + row) * p.r);
@@ -233,24 +239,27 @@ __global__ void __launch_bounds__(kThreads) k12_few_adapters(const __grid_consta
 }
 
 template <int NT>
-cudaError_t launch_few(const Params &p, int sms, cudaStream_t s) {
+int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   using F = Few<NT>;
+  Planes planes;
+  if (!make_planes(planes, p.w, p.N, p.K)) return WC_ERR_CUDA;
   if (cudaFuncSetAttribute(k12_few_adapters<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::kSmem)) != cudaSuccess)
-    return cudaGetLastError();
-  // CTAs that split K: as many as run at once (4 an SM), while each keeps
-  // a ring's worth of units
-  const uint32_t blocks = p.N / (kRows * kWarps), units = p.K / kUnit;
+    return WC_ERR_CUDA;
+  // CTAs that split K: as many as run at once (3 an SM), while each fills
+  // its ring
+  const uint32_t blocks = p.N / kSubRows, units = p.K / kUnit;
   uint32_t csize = 1;
-  while (csize < 8 && blocks * csize * 2 <= 4u * uint32_t(sms) && units >= 2 * csize * F::kDepth) csize *= 2;
-  return launch(k12_few_adapters<NT>, dim3(blocks * csize), csize, F::kSmem, s, true, p, csize);
+  while (csize < 8 && blocks * csize * 2 <= 3u * uint32_t(sms) && units >= 4 * csize * kDepth) csize *= 2;
+  return launch(k12_few_adapters<NT>, dim3(blocks * csize), kThreads, csize, F::kSmem, s, true, p, planes, csize) == cudaSuccess
+             ? WC_OK : WC_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
 // More tokens: Y = the adapters' part (zero for a token without one).  A warp
 // takes 16 rows of N and 32 tokens; t enters as three bf16 numbers.
-__global__ void __launch_bounds__(kThreads) k12_adapter_expand(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kSideThreads) k12_adapter_expand(const __grid_constant__ Params p) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t n0 = (blockIdx.y * kWarps + warp) * kRows, m0 = 32 * blockIdx.x;
+  const uint32_t n0 = (blockIdx.y * kSideWarps + warp) * kRows, m0 = 32 * blockIdx.x;
   int32_t ad = -1;
   if (m0 + lane < p.M) ad = p.adapter[m0 + lane];
   if (ad < 0 || ad >= int32_t(p.L)) ad = -1;
@@ -321,7 +330,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
     return WC_ERR_INVALID_ARG;
   if (!aligned(d_adapter, 4) || !aligned(d_a, 16) || !aligned(d_b, 16) || !aligned(d_scale, 4) || !aligned(d_work, 16))
     return WC_ERR_INVALID_ARG;
-  if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > kMaxK || N / (kRows * kWarps) > 65535 || M > 0x7FFFFFFFu)
+  if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > kMaxK || N / (kRows * kSideWarps) > 65535 || M > 0x7FFFFFFFu)
     return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_linear_adapters_work_bytes(M, r)) return WC_ERR_CAPACITY;
   const int sms = wc12l::device_sms();
@@ -346,12 +355,12 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   {
     const uint32_t tiles = (M + 7) / 8, ranks = (r + 15) / 16, z = M < 8 ? M : 8;
     uint32_t csize = 1;  // CTAs that split K: until each SM has two, while a warp has two pieces
-    while (csize < 8 && tiles * ranks * csize < 2u * uint32_t(sms) && K / 64 >= 4 * csize * kWarps) csize *= 2;
-    if (launch(k12_adapter_shrink, dim3(tiles * csize, ranks, z), csize, 0, s, false, p, csize) != cudaSuccess)
+    while (csize < 8 && tiles * ranks * csize < 2u * uint32_t(sms) && K / 64 >= 4 * csize * kSideWarps) csize *= 2;
+    if (launch(k12_adapter_shrink, dim3(tiles * csize, ranks, z), kSideThreads, csize, 0, s, false, p, csize) != cudaSuccess)
       return WC_ERR_CUDA;
   }
-  if (M <= kFewTokens) return (M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s)) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
-  if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kWarps)), 1, 0, s, true, p) != cudaSuccess)
+  if (M <= kFewTokens) return M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s);
+  if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kSideWarps)), kSideThreads, 1, 0, s, true, p) != cudaSuccess)
     return WC_ERR_CUDA;
   return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, true, d_status, stream);
 }

@@ -6,19 +6,19 @@
 //   out[t] = sum over e in S_t of p_e D_e (silu(G_e x_t) * U_e x_t)
 //
 // The bytes of the chosen experts' weights bound it, so both kernels stream
-// them through registers (wc12_few.cuh), 8 of the tokens that chose an expert
-// at a time (an item; more than 8 are rare, and read the weights again, from
+// them through a ring (wc12_few.cuh), 8 of the tokens that chose an expert at
+// a time (an item; more than 8 are rare, and read the weights again, from
 // L2):
-//   * k12_moe_up: the CTAs go through (item, 16 rows of F) one after another,
-//     as many as run at once, so that the routing is found once and the
-//     copies in flight run on from one to the next.  A warp takes a part of H
-//     for the 16 rows of G_e and the same of U_e, and p_e silu(g) u is
-//     written as the sum of two bf16 numbers (16 bits: rounding it to 8 would
-//     cost the output as much again as its own rounding to bf16);
-//   * k12_moe_down: a cluster takes rows of the output and walks through D_e
-//     of every item as through one long row, whose parts its warps take.  The
-//     weighted sum over experts is part of the product's sum: no atomics, one
-//     rounding, one write.
+//   * k12_moe_up: a job is 64 rows of G_e and the same of U_e for one item.
+//     With many jobs as many CTAs as run at once go through them, so that the
+//     routing is found once and the ring runs on from one to the next; with
+//     few, the CTAs of a cluster split H.  p_e silu(g) u is written as the sum
+//     of two bf16 numbers (16 bits: rounding it to 8 would cost the output as
+//     much again as its own rounding to bf16);
+//   * k12_moe_down: a cluster takes 64 rows of the output and walks through
+//     D_e of every item as through one long row, whose parts its CTAs take.
+//     The weighted sum over experts is part of the product's sum: no atomics,
+//     one rounding, one write.
 // Both find the experts from the logits themselves, a warp a token (a few
 // hundred logits), instead of waiting for a third kernel; the second starts
 // while the first one ends (programmatic dependent launch) and by then has
@@ -26,10 +26,6 @@
 #include <cstdint>
 
 #include "wc12_few.cuh"
-
-namespace wc12l {
-int device_sms();
-}
 
 namespace wc12m {
 
@@ -65,7 +61,7 @@ struct Route {
 };
 // while it is found (in shared memory that the ring takes later)
 struct RouteScratch {
-  uint32_t key[kWarps][kMaxExperts];
+  uint32_t key[kThreads / 32][kMaxExperts];
   uint32_t who[kMaxExperts];    // the tokens that chose each expert, a bit each
   uint16_t first[kMaxExperts];  // their first place in pair[]
 };
@@ -82,7 +78,7 @@ __device__ void route(Route &r, RouteScratch &w, const Params &p) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (uint32_t e = tid; e < p.E; e += kThreads) w.who[e] = 0;
   __syncthreads();
-  for (uint32_t m = warp; m < p.T; m += kWarps) {
+  for (uint32_t m = warp; m < p.T; m += kThreads / 32) {
     const float *l = p.logits + uint64_t(m) * p.E;
     uint32_t *key = w.key[warp];
     // each lane looks at its own experts only: no barrier needed
@@ -156,201 +152,223 @@ __device__ void route(Route &r, RouteScratch &w, const Params &p) {
 }
 
 // ---------------------------------------------------------------------------
+constexpr uint32_t align128(uint32_t v) { return (v + 127) / 128 * 128; }
+
 struct Up {
-  using R = Ring<2, 1, 1>;
-  static constexpr uint32_t kDepth = 3;
-  static constexpr uint32_t kSums = 8 * kRedTok;  // floats a warp and matrix
-  static constexpr uint32_t kRoute = kWarps * kDepth * R::kBytes;
-  static constexpr uint32_t kLists = (kRoute + uint32_t(sizeof(Route)) + 15) / 16 * 16;
-  static constexpr uint32_t kRed = kLists + kWarps * kListCap * 4;
-  static constexpr uint32_t kSmem = kRed + kWarps * 2 * kSums * 4;
+  static constexpr uint32_t kStage = stage_bytes(8);
+  static constexpr uint32_t kOwn = own_words(8);  // words of a warp: its list, then its sums
+  static constexpr uint32_t kRoute = kDepth * kStage;
+  static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
+  static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
+  static constexpr uint32_t kSmem = kBars + sizeof(Bars);
 };
 static_assert(sizeof(RouteScratch) <= Up::kRoute, "scratch");
 
-__global__ void __launch_bounds__(kThreads) k12_moe_up(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant__ Params p,
+                                                          const __grid_constant__ Planes planes, uint32_t csize) {
   launch_dependents();
-  extern __shared__ __align__(16) uint8_t dyn[];
-  Route &route_s = *reinterpret_cast<Route *>(dyn + Up::kRoute);
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  extern __shared__ __align__(128) uint8_t dyn[];
+  Route &r = *reinterpret_cast<Route *>(dyn + Up::kRoute);
+  Bars &bars = *reinterpret_cast<Bars *>(dyn + Up::kBars);
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % csize, first = blockIdx.x / csize, clusters = gridDim.x / csize;
   View v;
   open_planes(v, p.gate_up, uint64_t(p.E) * 2 * p.F * p.H);
-  const bool ok = open_header(v, p.gate_up, p.gate_up_bytes);
-  route(route_s, *reinterpret_cast<RouteScratch *>(dyn), p);
+  const bool ok = open_header(v, p.gate_up, p.gate_up_bytes);  // the same for every thread
+  if (tid == 0) bars_init(bars);
+  route(r, *reinterpret_cast<RouteScratch *>(dyn), p);
   if (!ok) {
     if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
     return;
   }
-  const uint32_t K = p.H, units = K / kUnit, u0 = units * warp / kWarps, u1 = units * (warp + 1) / kWarps;
-  const uint32_t groups = p.F / kRows, jobs = route_s.items * groups;
-  // rows of job j: 16 of G_e, and the same of U_e
-  auto row_of = [&](uint32_t job, uint32_t which) {
-    const uint32_t item = job / groups;
-    return (uint64_t(route_s.item_e[item]) * 2 + which) * p.F + (job - item * groups) * kRows;
-  };
-  // copies run ahead of the products, over the ends of jobs
-  uint32_t load_job = blockIdx.x, load_u = u0;
-  const uint8_t *pi[2], *pl[2];
-  const uint16_t *px = p.x;
-  uint32_t live = 0;
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * Up::kDepth * Up::R::kBytes;
-  auto load = [&](uint32_t slot) {
-    if (load_job < jobs && u0 < u1) {
-      if (load_u == u0) {
-#pragma unroll
-        for (uint32_t w = 0; w < 2; w++) {
-          const uint64_t at = (row_of(load_job, w) + g) * K + u0 * kUnit;
-          pi[w] = v.idx + at / 2 + 8 * t;
-          pl[w] = v.lo + at + 16 * t;
+  const uint32_t K = p.H, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
+  const uint32_t tiles = p.F / kSubRows, jobs = r.items * tiles, ring = smem_u32(dyn);
+  float *red = reinterpret_cast<float *>(dyn + Up::kLists);
+  if (warp == kWarps) {
+    fence_async();  // the routing's scratch was in the ring
+    uint32_t s = 0;
+    bool alive = true;
+    for (uint32_t job = first; alive && job < jobs; job += clusters) {
+      const uint32_t item = job / tiles, n = r.item_n[item];
+      const uint32_t row = uint32_t(r.item_e[item]) * 2 * p.F + (job - item * tiles) * kSubRows;
+      const uint16_t *px = p.x;
+      if (lane < n) px += uint64_t(r.pair[r.item_first[item] + lane] / p.k) * K;
+      for (uint32_t u = u0; u < u1; u++, s++) {
+        if (s >= kDepth && !bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) {
+          alive = false;
+          break;
         }
-        const uint32_t item = load_job / groups;
-        live = g < route_s.item_n[item];
-        const uint32_t m = live ? route_s.pair[route_s.item_first[item] + g] / p.k : 0u;
-        px = p.x + uint64_t(m) * K + u0 * kUnit + 16 * t;
-      }
-      Up::R::load(ring + slot * Up::R::kBytes, lane, pi, pl, K, &px, live, 1, 0);
-#pragma unroll
-      for (uint32_t w = 0; w < 2; w++) {
-        pi[w] += kUnit / 2;
-        pl[w] += kUnit;
-      }
-      px += kUnit;
-      if (++load_u == u1) {
-        load_u = u0;
-        load_job += gridDim.x;
+        uint64_t *full = &bars.full[s % kDepth];
+        const uint32_t slot = ring + s % kDepth * Up::kStage;
+        if (lane == 0) {
+          bar_expect(full, 2 * kSubBytes + n * 2 * kUnit);
+          load_subtile(slot, planes, u * kUnit, row, full);
+          load_subtile(slot + kSubBytes, planes, u * kUnit, row + p.F, full);
+        }
+        __syncwarp();
+        if (lane < n) load_row(slot + 2 * kSubBytes + lane * kXRow, px + u * kUnit, 2 * kUnit, full);
       }
     }
-    copies_commit();
+    // no copy is in flight when the CTA ends
+    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+    if (csize > 1 && first < jobs) {  // with the others' barriers
+      cluster_sync();
+      cluster_sync();
+    }
+    return;
+  }
+  const uint32_t group = warp & 3, sub = warp >> 2;  // sub 0: G_e, 1: U_e
+  auto row_of = [&](uint32_t job) {
+    const uint32_t item = job / tiles;
+    return (uint64_t(r.item_e[item]) * 2 + sub) * p.F + (job - item * tiles) * kSubRows + kRows * group;
   };
-#pragma unroll
-  for (uint32_t i = 0; i < Up::kDepth; i++) load(i);
   // the exceptions of a job are in flight during the one before, their
   // offsets during the one before that
-  Window now[2], next[2];
-  auto offsets = [&](Window *w, uint32_t job) {
-    if (v.ne > 0 && job < jobs)
-      for (uint32_t i = 0; i < 2; i++) window_offsets(w[i], v.exc_off, row_of(job, i), K, lane);
+  Window now, next;
+  auto offsets = [&](Window &w, uint32_t job) {
+    if (v.ne > 0 && job < jobs) window_offsets(w, v.exc_off, row_of(job), K, lane);
   };
-  auto entries = [&](Window *w, uint32_t job) {
-    if (v.ne > 0 && job < jobs)
-      for (uint32_t i = 0; i < 2; i++) window_entries(w[i], v, lane);
+  auto entries = [&](Window &w, uint32_t job) {
+    if (v.ne > 0 && job < jobs) window_entries(w, v, lane);
   };
-  offsets(now, blockIdx.x);
-  offsets(next, blockIdx.x + gridDim.x);
-  entries(now, blockIdx.x);
+  offsets(now, first);
+  offsets(next, first + clusters);
+  entries(now, first);
   Exceptions x;
-  x.list = reinterpret_cast<uint32_t *>(dyn + Up::kLists) + warp * kListCap;
-  float *red = reinterpret_cast<float *>(dyn + Up::kRed);
+  x.list = reinterpret_cast<uint32_t *>(dyn + Up::kLists) + warp * Up::kOwn;
   const uint64_t plane = uint64_t(p.T) * p.k * p.F;
-  uint32_t slot = 0;
-  for (uint32_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+  uint32_t s = 0;
+  bool alive = true;
+  for (uint32_t job = first; job < jobs; job += clusters) {
+    const uint64_t row0 = row_of(job);
     exceptions_reset(x);
     if (v.ne > 0) {
-      for (uint32_t i = 0; i < 2; i++) window_keep(x, now[i], v, row_of(job, i), K, i, u0, u1, lane, p.status);
+      window_keep(x, now, v, row0, K, u0, u1, 1, lane, p.status);
       exceptions_ready(x, lane);
     }
-    now[0] = next[0];
-    now[1] = next[1];
-    entries(now, job + gridDim.x);
-    offsets(next, job + 2 * gridDim.x);
-    const uint64_t row_g[2] = {row_of(job, 0) + g, row_of(job, 1) + g};
-    float tot[2][1][4] = {};
-    for (uint32_t u = u0; u < u1; u++) {
-      copies_wait<Up::kDepth - 1>();
-      unit_product<2, 1, 1>(tot, ring + slot * Up::R::kBytes, v.book, v, 1, x, u, row_g, K, lane);
-      load(slot);
-      slot = slot + 1 == Up::kDepth ? 0 : slot + 1;
+    now = next;
+    entries(now, job + clusters);
+    offsets(next, job + 2 * clusters);
+    float tot[1][4] = {};
+    for (uint32_t u = u0; alive && u < u1; u++, s++) {
+      alive = bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status);
+      if (!alive) break;
+      const uint32_t slot = ring + s % kDepth * Up::kStage, at = slot + sub * kSubBytes;
+      unit_product<1, 1>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64, slot + 2 * kSubBytes, v.book, v, x,
+                         u, row0 + (lane >> 2), K, lane);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
     }
-    put_sums<1>(red + 2 * warp * Up::kSums, tot[0], lane);
-    put_sums<1>(red + (2 * warp + 1) * Up::kSums, tot[1], lane);
-    __syncthreads();
-    const uint32_t item = job / groups, row = tid % kRows, c = tid / kRows;  // 16 x 8 threads
-    if (c < route_s.item_n[item]) {
+    __syncwarp();
+    put_sums<1>(red + warp * Up::kOwn, tot, lane);
+    if (csize > 1) cluster_sync(); else consumers_sync();
+    const uint32_t item = job / tiles, n = r.item_n[item];
+    for (uint32_t o = tid + rank * kConsumers; o < n * kSubRows; o += kConsumers * csize) {
+      const uint32_t row = o % kSubRows, c = o / kSubRows;
+      const float *from = red + row / kRows * Up::kOwn + c * kRedTok + row % kRows;
       float gate = 0.0f, up = 0.0f;
-#pragma unroll
-      for (uint32_t w = 0; w < kWarps; w++) {
-        gate += red[2 * w * Up::kSums + c * kRedTok + row];
-        up += red[(2 * w + 1) * Up::kSums + c * kRedTok + row];
+      for (uint32_t i = 0; i < csize; i++) {
+        gate += csize > 1 ? cluster_load(from, i) : from[0];
+        up += csize > 1 ? cluster_load(from + 4 * Up::kOwn, i) : from[4 * Up::kOwn];
       }
-      const uint32_t pair = route_s.pair[route_s.item_first[item] + c];
-      const float h = gate / (1.0f + expf(-gate)) * up * route_s.p[pair / p.k][pair % p.k];
+      const uint32_t pair = r.pair[r.item_first[item] + c];
+      const float h = gate / (1.0f + expf(-gate)) * up * r.p[pair / p.k][pair % p.k];
       // two bf16 numbers, each rounded to nearest: off by at most 2^-18
-      uint16_t *dst = p.hs + uint64_t(pair) * p.F + (job - item * groups) * kRows + row;
+      uint16_t *dst = p.hs + uint64_t(pair) * p.F + (job - item * tiles) * kSubRows + row;
       const uint32_t hi = bf16_bits(h);
       dst[0] = uint16_t(hi);
       dst[plane] = uint16_t((hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(h - __uint_as_float(hi << 16)));
     }
-    __syncthreads();  // red is read until here
+    if (csize > 1) cluster_sync(); else consumers_sync();  // the sums are read until here
   }
-  copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// A warp has the part `part` of 2^sbits of its cluster rank's units, for one
-// of the CTA's 4 >> sbits groups of 16 rows.
+// A stage's two subtiles are successive ranges of F.
 struct Down {
-  using R = Ring<1, 1, 2>;
-  static constexpr uint32_t kDepth = 3;
-  static constexpr uint32_t kRoute = kWarps * kDepth * R::kBytes;
-  static constexpr uint32_t kLists = (kRoute + uint32_t(sizeof(Route)) + 15) / 16 * 16;
-  static constexpr uint32_t kAcc = kLists + kWarps * kListCap * 4;
+  static constexpr uint32_t kStage = stage_bytes(16);
+  static constexpr uint32_t kRoute = kDepth * kStage;
+  static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
+  static constexpr uint32_t kBars = kLists + kWarps * kListCap * 4;
+  static constexpr uint32_t kAcc = align128(kBars + uint32_t(sizeof(Bars)));
   static __host__ __device__ uint32_t smem(uint32_t T) { return kAcc + kWarps * T * kRedTok * 4; }
 };
 static_assert(sizeof(RouteScratch) <= Down::kRoute, "scratch");
 
-__global__ void __launch_bounds__(kThreads) k12_moe_down(const __grid_constant__ Params p, uint32_t csize,
-                                                        uint32_t sbits) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  Route &route_s = *reinterpret_cast<Route *>(dyn + Down::kRoute);
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = blockIdx.x % csize, rows = kRows * kWarps >> sbits, n0 = blockIdx.x / csize * rows;
-  const uint32_t part = (rank << sbits) + (warp & ((1u << sbits) - 1)), parts = csize << sbits;
-  const uint32_t row0 = n0 + kRows * (warp >> sbits);
+__global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constant__ Params p,
+                                                            const __grid_constant__ Planes planes, uint32_t csize) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  Route &r = *reinterpret_cast<Route *>(dyn + Down::kRoute);
+  Bars &bars = *reinterpret_cast<Bars *>(dyn + Down::kBars);
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kSubRows;
   View v;
   open_planes(v, p.down, uint64_t(p.E) * p.H * p.F);
-  const bool ok = open_header(v, p.down, p.down_bytes);
-  route(route_s, *reinterpret_cast<RouteScratch *>(dyn), p);
+  const bool ok = open_header(v, p.down, p.down_bytes);  // the same for every thread
+  if (tid == 0) bars_init(bars);
   float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
-  for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
-  if (ok) {
-    // the items' units one after another; this warp's: [q0, q1)
-    const uint32_t K = p.F, units = K / kUnit, all = route_s.items * units;
-    const uint32_t q0 = uint32_t(uint64_t(all) * part / parts), q1 = uint32_t(uint64_t(all) * (part + 1) / parts);
+  if (warp < kWarps)
+    for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
+  route(r, *reinterpret_cast<RouteScratch *>(dyn), p);
+  // the items' stages one after another; this CTA's: [q0, q1)
+  const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2, all = r.items * per, ring = smem_u32(dyn);
+  const uint32_t q0 = ok ? uint32_t(uint64_t(all) * rank / csize) : 0u, q1 = ok ? uint32_t(uint64_t(all) * (rank + 1) / csize) : 0u;
+  const uint32_t first = q0 / per, st0 = q0 - first * per;  // item, stage of it
+  if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
+  if (warp == kWarps) {
+    fence_async();  // the routing's scratch was in the ring
     const uint64_t plane = uint64_t(p.T) * p.k * p.F;
-    auto row_of = [&](uint32_t item) { return uint64_t(route_s.item_e[item]) * p.H + row0; };
-    uint32_t load_q = q0, load_item = q0 / units, load_u = q0 - load_item * units;
-    const uint8_t *pi = nullptr, *pl = nullptr;
-    const uint16_t *px = p.hs;
-    uint32_t live = 0;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * Down::kDepth * Down::R::kBytes;
-    // the weights of the first units are on their way before hs is waited
-    // for, its values follow
-    auto load = [&](uint32_t slot, bool weights, bool values) {
-      if (load_q < q1) {
-        if (load_q == q0 || load_u == 0) {
-          const uint64_t at = (row_of(load_item) + g) * K + load_u * kUnit;
-          pi = v.idx + at / 2 + 8 * t;
-          pl = v.lo + at + 16 * t;
-          live = g < route_s.item_n[load_item];
-          const uint32_t pair = live ? route_s.pair[route_s.item_first[load_item] + g] : 0u;
-          px = p.hs + uint64_t(pair) * K + load_u * kUnit + 16 * t;
-        }
-        const uint32_t to = ring + slot * Down::R::kBytes;
-        if (weights) Down::R::load_weights(to, lane, &pi, &pl, K);
-        if (values) Down::R::load_values(to, lane, &px, live, 1, plane);
-        pi += kUnit / 2;
-        pl += kUnit;
-        px += kUnit;
-        load_q++;
-        if (++load_u == units) {
-          load_u = 0;
-          load_item++;
-        }
+    uint32_t item = first, st = st0;
+    auto subs_of = [&](uint32_t st) { return 2 * st + 1 < units ? 2u : 1u; };
+    auto weights = [&](uint32_t s, uint32_t item, uint32_t st) {
+      uint64_t *full = &bars.full[s % kDepth];
+      const uint32_t slot = ring + s % kDepth * Down::kStage, subs = subs_of(st);
+      const uint32_t row = uint32_t(r.item_e[item]) * p.H + n0;
+      if (lane == 0) {
+        bar_expect(full, subs * (kSubBytes + r.item_n[item] * 4 * kUnit));
+        for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (2 * st + i) * kUnit, row, full);
+      }
+      __syncwarp();
+    };
+    auto values = [&](uint32_t s, uint32_t item, uint32_t st) {  // lanes 0-7: the first plane, 8-15: the second
+      const uint32_t i = lane & 7;
+      if (lane < 16 && i < r.item_n[item])
+        load_row(ring + s % kDepth * Down::kStage + 2 * kSubBytes + lane * kXRow,
+                 p.hs + (lane >> 3) * plane + uint64_t(r.pair[r.item_first[item] + i]) * K + 2 * st * kUnit,
+                 subs_of(st) * 2 * kUnit, &bars.full[s % kDepth]);
+    };
+    auto step = [&] {
+      if (++st == per) {
+        st = 0;
+        item++;
       }
     };
-    uint32_t item = load_item, u = load_u;
-#pragma unroll
-    for (uint32_t i = 0; i < Down::kDepth; i++) load(i, true, false);
-    const uint32_t last = q0 < q1 ? (q1 - 1) / units : 0u;
+    // the weights of the first stages are on their way before hs is waited
+    // for, its values follow
+    uint32_t s = 0;
+    for (uint32_t q = q0; q < q1 && s < kDepth; q++, s++) {
+      weights(s, item, st);
+      step();
+    }
+    wait_prerequisites();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    item = first;
+    st = st0;
+    for (uint32_t i = 0; i < s; i++) {
+      values(i, item, st);
+      step();
+    }
+    for (uint32_t q = q0 + s; q < q1; q++, s++) {
+      if (!bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) break;
+      weights(s, item, st);
+      values(s, item, st);
+      step();
+    }
+    // no copy is in flight when the CTA ends
+    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+  } else if (q0 < q1) {
+    const uint32_t group = warp & 3, sub = warp >> 2, row0 = n0 + kRows * group, last = (q1 - 1) / per;
+    auto row_of = [&](uint32_t item) { return uint64_t(r.item_e[item]) * p.H + row0; };
     Window now, next;
     auto offsets = [&](Window &w, uint32_t i) {
       if (v.ne > 0 && i <= last) window_offsets(w, v.exc_off, row_of(i), K, lane);
@@ -358,70 +376,58 @@ __global__ void __launch_bounds__(kThreads) k12_moe_down(const __grid_constant__
     auto entries = [&](Window &w, uint32_t i) {
       if (v.ne > 0 && i <= last) window_entries(w, v, lane);
     };
-    if (q0 < q1) {
-      offsets(now, item);
-      offsets(next, item + 1);
-      entries(now, item);
-    }
-    wait_prerequisites();  // hs
-    load_q = q0;
-    load_item = item;
-    load_u = u;
-#pragma unroll
-    for (uint32_t i = 0; i < Down::kDepth; i++) {
-      load(i, false, true);
-      copies_commit();
-    }
+    offsets(now, first);
+    offsets(next, first + 1);
+    entries(now, first);
     Exceptions x;
     x.list = reinterpret_cast<uint32_t *>(dyn + Down::kLists) + warp * kListCap;
-    uint32_t slot = 0;
-    for (uint32_t q = q0; q < q1; item++, u = 0) {
-      const uint32_t end = q1 - q < units - u ? u + (q1 - q) : units;
+    uint32_t s = 0, st = st0;
+    bool alive = true;
+    for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
+      const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
       exceptions_reset(x);
       if (v.ne > 0) {
-        window_keep(x, now, v, row_of(item), K, 0, u, end, lane, p.status);
+        window_keep(x, now, v, row_of(item), K, 2 * st + sub, 2 * end, 2, lane, p.status);
         exceptions_ready(x, lane);
       }
       now = next;
       entries(now, item + 1);
       offsets(next, item + 2);
-      const uint64_t row_g = row_of(item) + g;
-      float tot[1][1][4] = {};
-      for (; u < end; u++, q++) {
-        copies_wait<Down::kDepth - 1>();
-        unit_product<1, 1, 2>(tot, ring + slot * Down::R::kBytes, v.book, v, 1, x, u, &row_g, K, lane);
-        load(slot, true, true);
-        copies_commit();
-        slot = slot + 1 == Down::kDepth ? 0 : slot + 1;
+      float tot[1][4] = {};
+      for (; st < end; st++, q++, s++) {
+        alive = bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status);
+        if (!alive) break;
+        const uint32_t slot = ring + s % kDepth * Down::kStage, at = slot + sub * kSubBytes, u = 2 * st + sub;
+        if (u < units)
+          unit_product<1, 2>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64,
+                             slot + 2 * kSubBytes + sub * 2 * kUnit, v.book, v, x, u, row_of(item) + (lane >> 2), K, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
       }
       // columns to tokens; a token that did not choose the expert gets
       // nothing (not even zero times an infinite weight)
-      const uint32_t n = route_s.item_n[item], first = route_s.item_first[item];
+      const uint32_t n = r.item_n[item], from = r.item_first[item], g = lane >> 2, t = lane & 3;
 #pragma unroll
       for (uint32_t i = 0; i < 2; i++)
         if (2 * t + i < n) {
-          float *to = acc + route_s.pair[first + 2 * t + i] / p.k * kRedTok + g;
-          to[0] += tot[0][0][i];
-          to[8] += tot[0][0][2 + i];
+          float *to = acc + r.pair[from + 2 * t + i] / p.k * kRedTok + g;
+          to[0] += tot[0][i];
+          to[8] += tot[0][2 + i];
         }
     }
-    copies_wait<0>();
-  } else {
-    if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
-    wait_prerequisites();
   }
   if (csize > 1) cluster_sync(); else __syncthreads();
+  wait_prerequisites();
   if (ok) {
     const float *sums = reinterpret_cast<const float *>(dyn + Down::kAcc);
-    for (uint32_t o = tid + rank * kThreads; o < p.T * rows; o += kThreads * csize) {
-      const uint32_t row = o % rows, m = o / rows;
-      const float *from = sums + ((row / kRows << sbits) * p.T + m) * kRedTok + row % kRows;
+    for (uint32_t o = tid + rank * kThreads; o < p.T * kSubRows; o += kThreads * csize) {
+      const uint32_t row = o % kSubRows, m = o / kSubRows;
+      const float *from = sums + (row / kRows * p.T + m) * kRedTok + row % kRows;
       float sum = 0.0f;
-      for (uint32_t c = 0; c < csize; c++)
-        for (uint32_t i = 0; i < 1u << sbits; i++) {
-          const float *f = from + i * p.T * kRedTok;
-          sum += csize > 1 ? cluster_load(f, c) : *f;
-        }
+      for (uint32_t c = 0; c < csize; c++) {
+        if (csize > 1) sum += cluster_load(from, c) + cluster_load(from + 4 * p.T * kRedTok, c);
+        else sum = from[0] + from[4 * p.T * kRedTok];
+      }
       const uint64_t at = uint64_t(m) * p.H + n0 + row;
       if (p.wide) static_cast<float *>(p.out)[at] = sum;
       else static_cast<uint16_t *>(p.out)[at] = uint16_t(bf16_bits(sum));
@@ -477,23 +483,25 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
       cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&up_per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess || up_per_sm < 1)
     return WC_ERR_CUDA;
+  Planes up, down;
+  if (!make_planes(up, d_gate_up, uint64_t(E) * 2 * F, H) || !make_planes(down, d_down, uint64_t(E) * H, F)) return WC_ERR_CUDA;
   for (uint32_t m = 0; m < T; m += kMaxTokens) {
     p.T = T - m < kMaxTokens ? T - m : kMaxTokens;
     p.x = static_cast<const uint16_t *>(d_x) + uint64_t(m) * H;
     p.logits = d_logits + uint64_t(m) * E;
     p.out = static_cast<uint8_t *>(d_out) + uint64_t(m) * H * (p.wide ? 4 : 2);
-    // up: as many CTAs as run at once
-    const uint32_t pairs = p.T * k, jobs = pairs * (F / kRows), slots = uint32_t(sms * up_per_sm);
-    // down: CTAs that split the items (and, with few rows, warps that do),
-    // until about 4 CTAs an SM have work
-    uint32_t csize = 1, sbits = 0;
+    // up: clusters that split H until about 3 CTAs an SM have work; with
+    // more jobs than that, as many CTAs as run at once
+    const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows), slots = uint32_t(sms * up_per_sm);
+    uint32_t cu = 1;
+    while (cu < 8 && jobs * cu * 2 <= 3u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
+    // down: CTAs that split the items, the same
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
-    while (csize < 8 && H / 64 * csize * 2 <= 4u * uint32_t(sms) && some >= 2 * csize * Down::kDepth) csize *= 2;
-    while (sbits < 2 && ((H / 64 * csize) << (sbits + 1)) <= 4u * uint32_t(sms) &&
-           some >= (2 * csize << sbits) * Down::kDepth)
-      sbits++;
-    if (launch(k12_moe_up, dim3(jobs < slots ? jobs : slots), 1, Up::kSmem, s, false, p) != cudaSuccess) return WC_ERR_CUDA;
-    if (launch(k12_moe_down, dim3((H / 64 * csize) << sbits), csize, Down::smem(p.T), s, true, p, csize, sbits) != cudaSuccess)
+    uint32_t cd = 1;
+    while (cd < 8 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
+    if (launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < slots ? jobs : slots), kThreads, cu, Up::kSmem, s, false, p, up, cu) !=
+            cudaSuccess ||
+        launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;
   }
   return WC_OK;

@@ -16,12 +16,22 @@
 // token (column g) as 32 bytes.  Four products (steps) use them up, 4 values
 // of a lane's row each.
 //
-// Loads.  Each lane copies what it will use itself with cp.async into a ring
-// of shared memory, several units ahead: no register holds data in flight,
-// and nothing is exchanged, so that no barrier is needed anywhere in the
-// loop.  (Loading into registers instead left room for two stages only, and
-// the tokens' values then came from L2 at the moment of use: 25 us instead
-// of TIME1 for a 4096 x 4096 layer and one token.)
+// Loads.  A stage is two subtiles of 64 rows x 64 values of K, each the work
+// of 4 warps (16 rows each): two ranges of rows with the same values of K, or
+// the same rows with two successive ranges.  One warp brings the subtiles'
+// planes with TMA and the tokens' values with bulk copies, a row each, into a
+// ring of kDepth stages; 8 warps expand and multiply.  No barrier of the CTA
+// in the loop: a "full" and an "empty" mbarrier a stage.  The planes' boxes
+// are stored as rows of 32 and 64 bytes, so that the lanes that read together
+// read 128 bytes in a row; the tokens' rows are 272 bytes apart for the same
+// reason.  (First with loads to registers, 8-byte and 16-byte ones, two
+// stages ahead: 25 us for a 4096 x 4096 layer and one token, the tokens'
+// values being fetched from L2 at the moment of use.  Then with the same
+// pieces copied ahead by cp.async: 13 us; 56 us for 14336 x 4096 and 16
+// tokens, twice the instructions of the product itself.)
+//
+// Every wait is bounded and gives up once another thread has; the kernel then
+// reports WC_ERR_TIMEOUT, waits for its copies in flight and ends.
 //
 // Exceptions.  Their high bytes replace the codebook's in the fragments,
 // before the product, so that an output has the exact weights and nothing
@@ -34,20 +44,34 @@
 
 #include <cstdint>
 
+#include <cuda.h>
+
 #include "wc.h"
 #include "wc_split12.cuh"
+
+namespace wc12l {
+// k_split12_linear.cu: a 2-D tensor map; the device's SMs (0 on failure)
+bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
+              uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw,
+              CUtensorMapL2promotion l2);
+int device_sms();
+}  // namespace wc12l
 
 namespace wc12f {
 
 using wc12::kChunk;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                   // that multiply
+constexpr int kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32;   // and one that loads
 constexpr uint32_t kRows = 16;       // weight rows of a group
-constexpr uint32_t kUnit = 64;       // values of K of a unit
+constexpr uint32_t kSubRows = 64;    // of a subtile
+constexpr uint32_t kUnit = 64;       // values of K of a subtile
 constexpr uint32_t kMaxK = 1 << 16;  // a group's rows touch at most 17 chunks
 constexpr uint32_t kListCap = 256;   // exceptions a warp keeps
-constexpr uint32_t kRedTok = 20;     // floats a token's 16 sums take (padded: no bank conflicts)
+constexpr uint32_t kRedTok = 18;     // floats a token's 16 sums take (padded: few bank conflicts)
+constexpr uint32_t kDepth = 4;       // stages of the ring
+constexpr uint32_t kSpinLimit = 1u << 24;
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
 
@@ -126,23 +150,14 @@ __device__ __forceinline__ bool open_header(View &v, const uint8_t *w, uint64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Copies to shared memory: 8 or 16 bytes, of which `bytes` are read and the
-// rest zeroed.  The weights (cg) pass by L1; the tokens' values are kept
-// there, since the warps of an SM use the same ones.
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// The ring.
+constexpr uint32_t kIdxBytes = kSubRows * kUnit / 2, kLoBytes = kSubRows * kUnit;
+constexpr uint32_t kSubBytes = kIdxBytes + kLoBytes;
+constexpr uint32_t kXRow = 272;  // bytes from one token's values to the next one's
+// a stage with n rows of tokens' values, whose place it starts at 2 kSubBytes
+__host__ __device__ constexpr uint32_t stage_bytes(uint32_t n) { return (2 * kSubBytes + n * kXRow + 127) / 128 * 128; }
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint4 shared16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -154,48 +169,74 @@ __device__ __forceinline__ uint2 shared8(uint32_t a) {
   return v;
 }
 
-// A warp's ring slot: a unit of kGroups groups of 16 rows and of 8 kTiles
-// tokens, whose values are held in kParts planes (a value as the sum of
-// kParts bf16 numbers).  Pieces of 16 bytes a lane (low bytes of group r,
-// row half h; the tokens'), then of 8 (indices).
-template <int kGroups, int kTiles, int kParts>
-struct Ring {
-  static constexpr uint32_t kX = 2 * kGroups, kPieces = kX + 2 * kTiles * kParts;
-  static constexpr uint32_t kIdx = kPieces * 512, kBytes = kIdx + 2 * kGroups * 256;
+// A warp's own part of shared memory: its list of exceptions, then its sums.
+constexpr uint32_t own_words(uint32_t tokens) { return tokens * kRedTok > kListCap ? tokens * kRedTok : kListCap; }
 
-  // pi, pl: this lane's place in row g of each group; K: the row length
-  static __device__ __forceinline__ void load_weights(uint32_t slot, uint32_t lane, const uint8_t *const *pi,
-                                                      const uint8_t *const *pl, uint32_t K) {
-#pragma unroll
-    for (int r = 0; r < kGroups; r++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        copy16(slot + (2 * r + h) * 512 + lane * 16, pl[r] + h * (uint64_t(K) * 8));
-        copy8(slot + kIdx + (2 * r + h) * 256 + lane * 8, pi[r] + h * (uint64_t(K) * 4));
-      }
-  }
-  // px: the lane's token's values in each tile of 8 (live: bit set if there
-  // is one, tiles: the tiles that have any), planes `plane` values apart
-  static __device__ __forceinline__ void load_values(uint32_t slot, uint32_t lane, const uint16_t *const *px,
-                                                     uint32_t live, uint32_t tiles, uint64_t plane) {
-#pragma unroll
-    for (int i = 0; i < kTiles; i++) {
-      if (kTiles > 1 && !((tiles >> i) & 1u)) continue;
-#pragma unroll
-      for (int part = 0; part < kParts; part++)
-#pragma unroll
-        for (int q = 0; q < 2; q++)
-          copy16_or_zero(slot + (kX + 2 * (i * kParts + part) + q) * 512 + lane * 16, px[i] + part * plane + 8 * q,
-                         (live >> i) & 1u);
-    }
-  }
-  static __device__ __forceinline__ void load(uint32_t slot, uint32_t lane, const uint8_t *const *pi,
-                                              const uint8_t *const *pl, uint32_t K, const uint16_t *const *px,
-                                              uint32_t live, uint32_t tiles, uint64_t plane) {
-    load_weights(slot, lane, pi, pl, K);
-    load_values(slot, lane, px, live, tiles, plane);
-  }
+struct Bars {
+  uint64_t full[kDepth], empty[kDepth];
+  int failed;
 };
+// by one thread, before a barrier of the CTA
+__device__ __forceinline__ void bars_init(Bars &b) {
+  for (uint32_t i = 0; i < kDepth; i++) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&b.full[i])) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&b.empty[i])), "n"(kWarps) : "memory");
+  }
+  b.failed = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+// whether the phase of the given parity came to its end, for the whole warp
+__device__ __forceinline__ bool bar_wait(Bars &b, uint64_t *bar, uint32_t parity, bool heed_failure, int32_t *status) {
+  const uint32_t a = smem_u32(bar);
+  bool done = false;
+  for (uint32_t i = 0; i < kSpinLimit && !done; i++) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(parity)
+        : "memory");
+    done = r != 0;
+    if (!done && heed_failure && *static_cast<volatile int *>(&b.failed)) break;
+  }
+  if (__all_sync(0xffffffffu, done)) return true;
+  if (!*static_cast<volatile int *>(&b.failed)) report(status, WC_ERR_TIMEOUT);
+  *static_cast<volatile int *>(&b.failed) = 1;
+  return false;
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// a box of 64 rows of a plane, from byte x of row y on, into this CTA
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void load_row(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// what threads wrote to the ring before is done before a copy writes there
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A container's planes as TMA sees them.
+struct Planes {
+  CUtensorMap idx, lo;
+};
+__device__ __forceinline__ void load_subtile(uint32_t dst, const Planes &m, uint32_t k, uint32_t row, uint64_t *bar) {
+  load_box(dst, &m.idx, k / 2, row, bar);
+  load_box(dst + kIdxBytes, &m.lo, k, row, bar);
+}
+// all 8 multiplying warps
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   uint32_t d;
@@ -223,13 +264,12 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
 
 // ---------------------------------------------------------------------------
 // Exceptions.  An entry: high byte (bits 0-7), row of the group (8-11),
-// column of the unit (12-17), group (18), unit of the row (19-31).
-__device__ __forceinline__ uint32_t pack_exc(uint32_t unit, uint32_t group, uint32_t col, uint32_t row, uint32_t high) {
-  return high | (row << 8) | (col << 12) | (group << 18) | (unit << 19);
+// column of the unit (12-17), unit of the row (18-31).
+constexpr uint32_t kExcUnit = 18;
+__device__ __forceinline__ uint32_t pack_exc(uint32_t unit, uint32_t col, uint32_t row, uint32_t high) {
+  return high | (row << 8) | (col << 12) | (unit << kExcUnit);
 }
-__device__ __forceinline__ uint32_t exc_step(uint32_t e) {  // group and product (4 group + 0..3) that use it
-  return ((e >> 16) & 4u) | ((e >> 14) & 3u);
-}
+__device__ __forceinline__ uint32_t exc_step(uint32_t e) { return (e >> 14) & 3u; }  // the product that uses it
 // puts the entry's high byte into the A words of its step, in its lane
 __device__ __forceinline__ void patch(uint32_t *a, uint32_t e, uint32_t lane) {
   const uint32_t owner = ((e >> 8) & 7u) * 4 + ((e >> 16) & 3u);
@@ -277,9 +317,10 @@ struct Exceptions {
   uint32_t cnt, e;
   bool walk;
 };
-// Entries have come: keeps those of the group's units [u0, u1).
+// Entries have come: keeps those of the group's units u0, u0 + step .. (below
+// u1); step 1 or 2.
 __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, const View &v, uint64_t row0, uint32_t K,
-                                            uint32_t group, uint32_t u0, uint32_t u1, uint32_t lane, int32_t *status) {
+                                            uint32_t u0, uint32_t u1, uint32_t step, uint32_t lane, int32_t *status) {
   const uint64_t e0 = __shfl_sync(0xffffffffu, w.off, 0), e1 = __shfl_sync(0xffffffffu, w.off, 31);
   const uint64_t before = __shfl_up_sync(0xffffffffu, w.off, 1);
   if (__any_sync(0xffffffffu, (lane > 0 && w.off < before) || w.off > v.ne)) {
@@ -304,13 +345,13 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
       if (in && f >= v.n) report(status, WC_ERR_CORRUPT);
       in = in && f >= f0 && f - f0 < uint64_t(kRows) * K;
       const uint32_t lf = in ? uint32_t(f - f0) : 0u, row = lf / K, col = lf - row * K, u = col / kUnit;
-      in = in && u >= u0 && u < u1;
+      in = in && u >= u0 && u < u1 && ((u - u0) & (step - 1)) == 0;
       const uint32_t m = __ballot_sync(0xffffffffu, in);
       if (x.cnt + __popc(m) > kListCap) {
         x.walk = true;
         return;
       }
-      if (in) x.list[x.cnt + __popc(m & ((1u << lane) - 1u))] = pack_exc(u, group, col % kUnit, row, (val >> (8 * i)) & 0xFFu);
+      if (in) x.list[x.cnt + __popc(m & ((1u << lane) - 1u))] = pack_exc(u, col % kUnit, row, (val >> (8 * i)) & 0xFFu);
       x.cnt += __popc(m);
     }
   }
@@ -359,41 +400,39 @@ __device__ __forceinline__ void walk_patch(uint32_t *a, const View &v, uint64_t 
   }
 }
 
-// One unit of the ring: the products of its rows and tokens, added to tot.
-// The four products of a unit are added up in the tensor cores, units in
-// fp32 registers: the tensor cores cut off what their accumulator cannot
-// hold, so that long sums there drift toward zero.  Columns without a token
-// hold sums that the caller drops.
-template <int kGroups, int kTiles, int kParts>
-__device__ __forceinline__ void unit_product(float tot[kGroups][kTiles][4], uint32_t slot, uint4 book, const View &v,
-                                             uint32_t tiles, const Exceptions &x, uint32_t unit,
-                                             const uint64_t *row_g, uint32_t K, uint32_t lane) {
-  using R = Ring<kGroups, kTiles, kParts>;
-  float d[kGroups][kTiles][4];
+// A warp's 16 rows of a subtile times 8 kTiles tokens, added to tot.  sub: its
+// rows' start in the subtile's index plane; xs: the tokens' values, kParts
+// rows of 8 kTiles tokens each (a value held as the sum of kParts bf16
+// numbers).  The four products of a unit are added up in the tensor cores,
+// units in fp32 registers: the tensor cores cut off what their accumulator
+// cannot hold, so that long sums there drift toward zero.  Columns without a
+// token hold sums that the caller drops.  row_g: the lane's first row.
+template <int kTiles, int kParts>
+__device__ __forceinline__ void unit_product(float tot[kTiles][4], uint32_t idx_at, uint32_t lo_at, uint32_t xs, uint4 book,
+                                             const View &v, const Exceptions &x, uint32_t unit, uint64_t row_g,
+                                             uint32_t K, uint32_t lane) {
+  const uint32_t g = lane >> 2, t = lane & 3;
+  uint2 idx[2];
+  uint4 lo[2], xv[kTiles][kParts];
 #pragma unroll
-  for (int r = 0; r < kGroups; r++)
+  for (int h = 0; h < 2; h++) {
+    idx[h] = shared8(idx_at + (g + 8 * h) * 32 + 8 * t);
+    lo[h] = shared16(lo_at + (g + 8 * h) * 64 + 16 * t);
+  }
+  float d[kTiles][4];
 #pragma unroll
-    for (int i = 0; i < kTiles; i++) d[r][i][0] = d[r][i][1] = d[r][i][2] = d[r][i][3] = 0.0f;
+  for (int i = 0; i < kTiles; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
   // the unit's exceptions: lanes that hold one, steps that have one
   uint32_t hit = 0, steps = 0;
   if (x.walk) {
-    steps = 0xFFu;
+    steps = 0xFu;
+  } else if (x.cnt > 32) {
+    steps = 0xFu;
   } else if (x.cnt > 0) {
-    const bool mine = lane < x.cnt && (x.e >> 19) == unit;
+    const bool mine = lane < x.cnt && (x.e >> kExcUnit) == unit;
     hit = __ballot_sync(0xffffffffu, mine);
-    if (x.cnt > 32) steps = 0xFFu;
-    else if (hit) steps = __reduce_or_sync(0xffffffffu, mine ? 1u << exc_step(x.e) : 0u);
+    if (hit) steps = __reduce_or_sync(0xffffffffu, mine ? 1u << exc_step(x.e) : 0u);
   }
-  uint4 lo[kGroups][2];
-  uint2 idx[kGroups][2];
-#pragma unroll
-  for (int r = 0; r < kGroups; r++)
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      lo[r][h] = shared16(slot + (2 * r + h) * 512 + lane * 16);
-      idx[r][h] = shared8(slot + R::kIdx + (2 * r + h) * 256 + lane * 8);
-    }
-  uint4 xv[kTiles][kParts];
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     if ((s & 1) == 0) {  // 8 values of each token, for two steps
@@ -401,51 +440,44 @@ __device__ __forceinline__ void unit_product(float tot[kGroups][kTiles][4], uint
       for (int i = 0; i < kTiles; i++)
 #pragma unroll
         for (int part = 0; part < kParts; part++)
-          xv[i][part] = shared16(slot + (R::kX + 2 * (i * kParts + part) + (s >> 1)) * 512 + lane * 16);
+          xv[i][part] = shared16(xs + ((part * kTiles + i) * 8 + g) * kXRow + 32 * t + 8 * s);
     }
+    uint32_t a[4];
 #pragma unroll
-    for (int r = 0; r < kGroups; r++) {
-      uint32_t a[4];
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const uint32_t qw = s < 2 ? idx[r][h].x : idx[r][h].y;
-        const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
-        const uint32_t lw = s == 0 ? lo[r][h].x : s == 1 ? lo[r][h].y : s == 2 ? lo[r][h].z : lo[r][h].w;
-        const uint2 e = expand4(sel, up, book, lw);
-        a[h] = e.x;
-        a[h + 2] = e.y;
-      }
-      if ((steps >> (4 * r + s)) & 1u) {
-        if (x.walk) {
-          walk_patch(a, v, row_g[r] * K + kUnit * unit + 16 * (lane & 3u) + 4 * s, K);
-        } else if (x.cnt > 32) {
-          for (uint32_t i = 0; i < x.cnt; i += 32) {
-            const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0xFFFFFFFFu;
-            uint32_t rest = __ballot_sync(0xffffffffu, i + lane < x.cnt && (own >> 19) == unit && exc_step(own) == uint32_t(4 * r + s));
-            for (; rest; rest &= rest - 1) patch(a, __shfl_sync(0xffffffffu, own, __ffs(rest) - 1), lane);
-          }
-        } else {
-          for (uint32_t rest = hit; rest; rest &= rest - 1) {
-            const uint32_t e = __shfl_sync(0xffffffffu, x.e, __ffs(rest) - 1);
-            if (exc_step(e) == uint32_t(4 * r + s)) patch(a, e, lane);
-          }
+    for (int h = 0; h < 2; h++) {
+      const uint32_t qw = s < 2 ? idx[h].x : idx[h].y;
+      const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
+      const uint32_t lw = s == 0 ? lo[h].x : s == 1 ? lo[h].y : s == 2 ? lo[h].z : lo[h].w;
+      const uint2 e = expand4(sel, up, book, lw);
+      a[h] = e.x;
+      a[h + 2] = e.y;
+    }
+    if ((steps >> s) & 1u) {
+      if (x.walk) {
+        walk_patch(a, v, row_g * K + kUnit * unit + 16 * t + 4 * s, K);
+      } else if (x.cnt > 32) {
+        for (uint32_t i = 0; i < x.cnt; i += 32) {
+          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
+          uint32_t rest = __ballot_sync(0xffffffffu, i + lane < x.cnt && (own >> kExcUnit) == unit && exc_step(own) == uint32_t(s));
+          for (; rest; rest &= rest - 1) patch(a, __shfl_sync(0xffffffffu, own, __ffs(rest) - 1), lane);
+        }
+      } else {
+        for (uint32_t rest = hit; rest; rest &= rest - 1) {
+          const uint32_t e = __shfl_sync(0xffffffffu, x.e, __ffs(rest) - 1);
+          if (exc_step(e) == uint32_t(s)) patch(a, e, lane);
         }
       }
-#pragma unroll
-      for (int i = 0; i < kTiles; i++) {
-        if (kTiles > 1 && !((tiles >> i) & 1u)) continue;
-#pragma unroll
-        for (int part = 0; part < kParts; part++)
-          mma(d[r][i], a, s & 1 ? xv[i][part].z : xv[i][part].x, s & 1 ? xv[i][part].w : xv[i][part].y);
-      }
     }
-  }
-#pragma unroll
-  for (int r = 0; r < kGroups; r++)
 #pragma unroll
     for (int i = 0; i < kTiles; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) tot[r][i][j] += d[r][i][j];
+      for (int part = 0; part < kParts; part++)
+        mma(d[i], a, s & 1 ? xv[i][part].z : xv[i][part].x, s & 1 ? xv[i][part].w : xv[i][part].y);
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) tot[i][j] += d[i][j];
 }
 
 // A warp's sums of a group, [token][row] with kRedTok floats a token.
@@ -462,14 +494,25 @@ __device__ __forceinline__ void put_sums(float *red, const float tot[kTiles][4],
   }
 }
 
-// Launches a kernel of kThreads threads in clusters of `cluster` CTAs along
-// x; dependent: it may start while the kernel before it in the stream runs
+// The tensor maps of a rows x K container's planes: boxes of 64 rows x 64
+// values (the planes' 256-byte L2 promotion is what lets such narrow boxes
+// stream at the memory's rate).
+inline bool make_planes(Planes &m, const void *w, uint64_t rows, uint32_t K) {
+  const wc12::Lay L = wc12::lay(rows * K, 0);
+  const uint8_t *p = static_cast<const uint8_t *>(w);
+  return wc12l::make_map(&m.idx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p + L.off_idx, K / 2, rows, K / 2, kUnit / 2, kSubRows,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+         wc12l::make_map(&m.lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, p + L.off_lo, K, rows, K, kUnit, kSubRows,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// Launches a kernel in clusters of `cluster` CTAs along x; dependent: it may start while the kernel before it in the stream runs
 // (it waits with wait_prerequisites).
 template <class... Args>
-cudaError_t launch(void (*kernel)(Args...), dim3 grid, uint32_t cluster, uint32_t smem, cudaStream_t s, bool dependent, Args... args) {
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, uint32_t block, uint32_t cluster, uint32_t smem, cudaStream_t s, bool dependent, Args... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = grid;
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(block);
   c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at[2];
