@@ -134,23 +134,26 @@ __global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_
 // cluster split K.  A stage's two subtiles are successive ranges of K.
 template <int NT>
 struct Few {
-  static constexpr uint32_t kStage = stage_bytes(8 * NT);
-  static constexpr uint32_t kOwn = own_words(8 * NT);  // a warp's list, then its sums
+  static constexpr uint32_t kXBox = NT * 1024;  // 8 NT tokens' values of a unit
+  static constexpr uint32_t kStage = 2 * kSubBytes + 2 * kXBox;
+  static constexpr uint32_t kOwn = own_words(8 * NT);  // words of a warp: its list, then its sums
   static constexpr uint32_t kLists = kDepth * kStage;
   static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
-  static constexpr uint32_t kSmem = kBars + sizeof(Bars);
+  static constexpr uint32_t kSmem = 1024 + kBars + sizeof(Bars);  // 1024: the boxes' swizzle counts from there
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 3) k12_few_adapters(const __grid_constant__ Params p,
-                                                                const __grid_constant__ Planes planes, uint32_t csize) {
+__global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_constant__ Params p,
+                                                                const __grid_constant__ Planes planes,
+                                                                const __grid_constant__ CUtensorMap tm_x, uint32_t csize) {
   using F = Few<NT>;
-  extern __shared__ __align__(128) uint8_t dyn[];
+  extern __shared__ __align__(128) uint8_t raw[];
+  uint8_t *dyn = raw + (1024 - smem_u32(raw) % 1024) % 1024;  // the same place in every CTA of the cluster
   Bars &bars = *reinterpret_cast<Bars *>(dyn + F::kBars);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kSubRows;
   const uint32_t K = p.K, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
-  const uint32_t stages = (u1 - u0 + 1) / 2, ring = smem_u32(dyn);
+  const uint32_t ring = smem_u32(dyn);
   View v;
   open_planes(v, p.w, uint64_t(p.N) * K);
   if (tid == 0) bars_init(bars);
@@ -158,54 +161,68 @@ __global__ void __launch_bounds__(kThreads, 3) k12_few_adapters(const __grid_con
   bool ok;
   float *red = reinterpret_cast<float *>(dyn + F::kLists);
   if (warp == kWarps) {
-    auto load = [&](uint32_t s) {
-      uint64_t *full = &bars.full[s % kDepth];
-      const uint32_t slot = ring + s % kDepth * F::kStage, u = u0 + 2 * s, subs = u + 1 < u1 ? 2 : 1;
+    Turn turn;
+    auto load = [&](uint32_t u) {
       if (lane == 0) {
-        bar_expect(full, subs * (kSubBytes + p.M * 2 * kUnit));
-        for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (u + i) * kUnit, n0, full);
+        uint64_t *full = &bars.full[turn.slot];
+        const uint32_t slot = ring + turn.slot * F::kStage, subs = u + 1 < u1 ? 2 : 1;
+        bar_expect(full, subs * (kSubBytes + F::kXBox));
+        for (uint32_t i = 0; i < subs; i++) {
+          load_subtile(slot + i * kSubBytes, planes, (u + i) * kUnit, n0, full);
+          load_box(slot + 2 * kSubBytes + i * F::kXBox, &tm_x, (u + i) * kUnit, 0, full);
+        }
       }
       __syncwarp();
-      if (lane < p.M) load_row(slot + 2 * kSubBytes + lane * kXRow, p.x + uint64_t(lane) * K + u * kUnit, subs * 2 * kUnit, full);
     };
-    uint32_t s = 0;
-    for (; s < kDepth && s < stages; s++) load(s);
+    uint32_t u = u0;
+    for (uint32_t i = 0; i < kDepth && u < u1; i++, u += 2, turn.next()) load(u);
     ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
-    for (; ok && s < stages; s++) {
-      if (!bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) break;
-      load(s);
+    for (; ok && u < u1; u += 2, turn.next()) {
+      if (!bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) break;
+      load(u);
     }
     // no copy is in flight when the CTA ends
-    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+    finish_copies(bars, turn, (u - u0) / 2, p.status);
   } else {
-    const uint32_t group = warp & 3, sub = warp >> 2, row0 = n0 + kRows * group;
+    const uint32_t row0 = n0 + kRows * warp;
     Window win;
     window_offsets(win, v.exc_off, row0, K, lane);
     Exceptions x;
     x.list = reinterpret_cast<uint32_t *>(dyn + F::kLists) + warp * F::kOwn;
     exceptions_reset(x);
     ok = open_header(v, p.w, p.w_bytes);
-    float tot[NT][4] = {};
+    float tot0[NT][4] = {}, tot1[NT][4] = {};
     if (ok) {
       if (v.ne > 0) {
         window_entries(win, v, lane);
-        window_keep(x, win, v, row0, K, u0 + sub, u1, 2, lane, p.status);
-        exceptions_ready(x, lane);
+        window_keep(x, win, v, row0, K, u0, u1, 1, 0, lane, p.status);
+        exceptions_ready(x, u0, lane);
       }
-      for (uint32_t s = 0; s < stages; s++) {
-        if (!bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status)) break;
-        const uint32_t slot = ring + s % kDepth * F::kStage, at = slot + sub * kSubBytes, u = u0 + 2 * s + sub;
-        if (u < u1)
-          unit_product<NT, 1>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64,
-                              slot + 2 * kSubBytes + sub * 2 * kUnit, v.book, v, x, u, row0 + (lane >> 2), K, lane);
+      const XAt xat = x_boxes(lane);
+      Turn turn;
+      for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
+        if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
+        const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
+        if (u + 1 < u1 && x.next > u + 1) {
+          stage_product<NT, 1, false>(tot0, tot1, slot, warp, xs, xs + F::kXBox, xat, 1024, v.book, lane);
+        } else {
+#pragma unroll 1
+          for (uint32_t i = 0; i < 2 && u + i < u1; i++)
+            subtile_product<NT, 1>(tot0, slot + i * kSubBytes, warp, xs + i * F::kXBox, xat, 1024, v, x, u + i, u + i,
+                                   row0 + (lane >> 2), K, lane);
+        }
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
+        if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
     } else if (blockIdx.x == 0 && tid == 0) {
       report(p.status, WC_ERR_CORRUPT);
     }
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) tot0[i][j] += tot1[i][j];
     __syncwarp();
-    put_sums<NT>(red + warp * F::kOwn, tot, lane);
+    put_sums<NT>(red + warp * F::kOwn, tot0, lane);
   }
   if (csize > 1) cluster_sync(); else __syncthreads();
   wait_prerequisites();  // t
@@ -215,10 +232,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_few_adapters(const __grid_con
       if (m >= p.M) break;
       const float *from = red + row / kRows * F::kOwn + m * kRedTok + row % kRows;
       float sum = 0.0f;
-      for (uint32_t c = 0; c < csize; c++) {
-        if (csize > 1) sum += cluster_load(from, c) + cluster_load(from + 4 * F::kOwn, c);
-        else sum = from[0] + from[4 * F::kOwn];
-      }
+      for (uint32_t c = 0; c < csize; c++) sum += csize > 1 ? cluster_load(from, c) : *from;
       const int32_t ad = p.adapter[m];
       if (ad >= 0 && ad < int32_t(p.L)) {
         const uint4 *pb = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad) * p.N + n0 + row) * p.r);
@@ -242,15 +256,20 @@ template <int NT>
 int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   using F = Few<NT>;
   Planes planes;
-  if (!make_planes(planes, p.w, p.N, p.K)) return WC_ERR_CUDA;
+  CUtensorMap tm_x;
+  if (!make_planes(planes, p.w, p.N, p.K) ||
+      !wc12l::make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, p.K, p.M, uint64_t(p.K) * 2, kUnit, 8 * NT,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+    return WC_ERR_CUDA;
   if (cudaFuncSetAttribute(k12_few_adapters<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::kSmem)) != cudaSuccess)
     return WC_ERR_CUDA;
-  // CTAs that split K: as many as run at once (3 an SM), while each fills
+  // CTAs that split K: as many as run at once (4 an SM), while each fills
   // its ring
   const uint32_t blocks = p.N / kSubRows, units = p.K / kUnit;
   uint32_t csize = 1;
-  while (csize < 8 && blocks * csize * 2 <= 3u * uint32_t(sms) && units >= 4 * csize * kDepth) csize *= 2;
-  return launch(k12_few_adapters<NT>, dim3(blocks * csize), kThreads, csize, F::kSmem, s, true, p, planes, csize) == cudaSuccess
+  while (csize < 8 && blocks * csize * 2 <= 4u * uint32_t(sms) && units >= 4 * csize * kDepth) csize *= 2;
+  return launch(k12_few_adapters<NT>, dim3(blocks * csize), kThreads, csize, F::kSmem, s, true, p, planes, tm_x, csize) ==
+                 cudaSuccess
              ? WC_OK : WC_ERR_CUDA;
 }
 

@@ -155,8 +155,8 @@ __device__ void route(Route &r, RouteScratch &w, const Params &p) {
 constexpr uint32_t align128(uint32_t v) { return (v + 127) / 128 * 128; }
 
 struct Up {
-  static constexpr uint32_t kStage = stage_bytes(8);
-  static constexpr uint32_t kOwn = own_words(8);  // words of a warp: its list, then its sums
+  static constexpr uint32_t kStage = align128(2 * kSubBytes + 8 * kXRow);
+  static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its list, then its sums of G_e and U_e
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
   static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
@@ -164,7 +164,17 @@ struct Up {
 };
 static_assert(sizeof(RouteScratch) <= Up::kRoute, "scratch");
 
-__global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant__ Params p,
+// p_e silu(gate) up as two bf16 numbers, each rounded to nearest: off by at
+// most 2^-18 of it
+__device__ __forceinline__ void put_gated(uint16_t *dst, uint64_t plane, float gate, float up, float weight) {
+  const float h = gate / (1.0f + expf(-gate)) * up * weight;
+  const uint32_t hi = bf16_bits(h);
+  dst[0] = uint16_t(hi);
+  dst[plane] = uint16_t((hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(h - __uint_as_float(hi << 16)));
+}
+
+// A stage's two subtiles: 64 rows of G_e and of U_e, the same values of H.
+__global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant__ Params p,
                                                           const __grid_constant__ Planes planes, uint32_t csize) {
   launch_dependents();
   extern __shared__ __align__(128) uint8_t dyn[];
@@ -183,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant_
   }
   const uint32_t K = p.H, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
   const uint32_t tiles = p.F / kSubRows, jobs = r.items * tiles, ring = smem_u32(dyn);
-  float *red = reinterpret_cast<float *>(dyn + Up::kLists);
+  Turn turn;
   if (warp == kWarps) {
     fence_async();  // the routing's scratch was in the ring
     uint32_t s = 0;
@@ -193,13 +203,13 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant_
       const uint32_t row = uint32_t(r.item_e[item]) * 2 * p.F + (job - item * tiles) * kSubRows;
       const uint16_t *px = p.x;
       if (lane < n) px += uint64_t(r.pair[r.item_first[item] + lane] / p.k) * K;
-      for (uint32_t u = u0; u < u1; u++, s++) {
-        if (s >= kDepth && !bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) {
+      for (uint32_t u = u0; u < u1; u++, s++, turn.next()) {
+        if (s >= kDepth && !bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) {
           alive = false;
           break;
         }
-        uint64_t *full = &bars.full[s % kDepth];
-        const uint32_t slot = ring + s % kDepth * Up::kStage;
+        uint64_t *full = &bars.full[turn.slot];
+        const uint32_t slot = ring + turn.slot * Up::kStage;
         if (lane == 0) {
           bar_expect(full, 2 * kSubBytes + n * 2 * kUnit);
           load_subtile(slot, planes, u * kUnit, row, full);
@@ -209,84 +219,98 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant_
         if (lane < n) load_row(slot + 2 * kSubBytes + lane * kXRow, px + u * kUnit, 2 * kUnit, full);
       }
     }
-    // no copy is in flight when the CTA ends
-    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+    finish_copies(bars, turn, s, p.status);
     if (csize > 1 && first < jobs) {  // with the others' barriers
       cluster_sync();
       cluster_sync();
     }
     return;
   }
-  const uint32_t group = warp & 3, sub = warp >> 2;  // sub 0: G_e, 1: U_e
-  auto row_of = [&](uint32_t job) {
+  auto row_of = [&](uint32_t job, uint32_t which) {
     const uint32_t item = job / tiles;
-    return (uint64_t(r.item_e[item]) * 2 + sub) * p.F + (job - item * tiles) * kSubRows + kRows * group;
+    return (uint64_t(r.item_e[item]) * 2 + which) * p.F + (job - item * tiles) * kSubRows + kRows * warp;
   };
   // the exceptions of a job are in flight during the one before, their
   // offsets during the one before that
-  Window now, next;
-  auto offsets = [&](Window &w, uint32_t job) {
-    if (v.ne > 0 && job < jobs) window_offsets(w, v.exc_off, row_of(job), K, lane);
+  Window now[2], next[2];
+  auto offsets = [&](Window *w, uint32_t job) {
+    if (v.ne > 0 && job < jobs)
+      for (uint32_t i = 0; i < 2; i++) window_offsets(w[i], v.exc_off, row_of(job, i), K, lane);
   };
-  auto entries = [&](Window &w, uint32_t job) {
-    if (v.ne > 0 && job < jobs) window_entries(w, v, lane);
+  auto entries = [&](Window *w, uint32_t job) {
+    if (v.ne > 0 && job < jobs)
+      for (uint32_t i = 0; i < 2; i++) window_entries(w[i], v, lane);
   };
   offsets(now, first);
   offsets(next, first + clusters);
   entries(now, first);
   Exceptions x;
   x.list = reinterpret_cast<uint32_t *>(dyn + Up::kLists) + warp * Up::kOwn;
+  float *sums = reinterpret_cast<float *>(dyn + Up::kLists);
   const uint64_t plane = uint64_t(p.T) * p.k * p.F;
-  uint32_t s = 0;
+  const XAt xat = x_rows(lane);
+  const uint32_t g = lane >> 2, t = lane & 3;
   bool alive = true;
   for (uint32_t job = first; job < jobs; job += clusters) {
-    const uint64_t row0 = row_of(job);
     exceptions_reset(x);
     if (v.ne > 0) {
-      window_keep(x, now, v, row0, K, u0, u1, 1, lane, p.status);
-      exceptions_ready(x, lane);
+#pragma unroll 1
+      for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
+      exceptions_ready(x, 2 * u0, lane);
     }
-    now = next;
+    now[0] = next[0];
+    now[1] = next[1];
     entries(now, job + clusters);
     offsets(next, job + 2 * clusters);
-    float tot[1][4] = {};
-    for (uint32_t u = u0; alive && u < u1; u++, s++) {
-      alive = bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status);
+    float gate[1][4] = {}, up[1][4] = {};
+    for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
+      alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
-      const uint32_t slot = ring + s % kDepth * Up::kStage, at = slot + sub * kSubBytes;
-      unit_product<1, 1>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64, slot + 2 * kSubBytes, v.book, v, x,
-                         u, row0 + (lane >> 2), K, lane);
+      const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
+      if (x.next > 2 * u + 1) {
+        stage_product<1, 1, true>(gate, up, slot, warp, xs, xs, xat, 0, v.book, lane);
+      } else {
+        subtile_product<1, 1>(gate, slot, warp, xs, xat, 0, v, x, 2 * u, u, row_of(job, 0) + g, K, lane);
+        subtile_product<1, 1>(up, slot + kSubBytes, warp, xs, xat, 0, v, x, 2 * u + 1, u, row_of(job, 1) + g, K, lane);
+      }
       __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
+      if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
+    }
+    const uint32_t item = job / tiles, n = r.item_n[item], from = r.item_first[item], f0 = (job - item * tiles) * kSubRows;
+    if (csize == 1) {  // a lane has both sums of its rows and columns
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++) {
+        const uint32_t c = 2 * t + (i & 1), row = f0 + kRows * warp + g + 8 * (i >> 1);
+        if (c < n) {
+          const uint32_t pair = r.pair[from + c];
+          put_gated(p.hs + uint64_t(pair) * p.F + row, plane, gate[0][i], up[0][i], r.p[pair / p.k][pair % p.k]);
+        }
+      }
+      continue;
     }
     __syncwarp();
-    put_sums<1>(red + warp * Up::kOwn, tot, lane);
-    if (csize > 1) cluster_sync(); else consumers_sync();
-    const uint32_t item = job / tiles, n = r.item_n[item];
+    put_sums<1>(sums + warp * Up::kOwn, gate, lane);
+    put_sums<1>(sums + warp * Up::kOwn + 8 * kRedTok, up, lane);
+    cluster_sync();
     for (uint32_t o = tid + rank * kConsumers; o < n * kSubRows; o += kConsumers * csize) {
       const uint32_t row = o % kSubRows, c = o / kSubRows;
-      const float *from = red + row / kRows * Up::kOwn + c * kRedTok + row % kRows;
-      float gate = 0.0f, up = 0.0f;
+      const float *at = sums + row / kRows * Up::kOwn + c * kRedTok + row % kRows;
+      float a = 0.0f, b = 0.0f;
       for (uint32_t i = 0; i < csize; i++) {
-        gate += csize > 1 ? cluster_load(from, i) : from[0];
-        up += csize > 1 ? cluster_load(from + 4 * Up::kOwn, i) : from[4 * Up::kOwn];
+        a += cluster_load(at, i);
+        b += cluster_load(at + 8 * kRedTok, i);
       }
-      const uint32_t pair = r.pair[r.item_first[item] + c];
-      const float h = gate / (1.0f + expf(-gate)) * up * r.p[pair / p.k][pair % p.k];
-      // two bf16 numbers, each rounded to nearest: off by at most 2^-18
-      uint16_t *dst = p.hs + uint64_t(pair) * p.F + (job - item * tiles) * kSubRows + row;
-      const uint32_t hi = bf16_bits(h);
-      dst[0] = uint16_t(hi);
-      dst[plane] = uint16_t((hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(h - __uint_as_float(hi << 16)));
+      const uint32_t pair = r.pair[from + c];
+      put_gated(p.hs + uint64_t(pair) * p.F + f0 + row, plane, a, b, r.p[pair / p.k][pair % p.k]);
     }
-    if (csize > 1) cluster_sync(); else consumers_sync();  // the sums are read until here
+    cluster_sync();  // the others' sums are read until here
   }
 }
 
 // ---------------------------------------------------------------------------
 // A stage's two subtiles are successive ranges of F.
 struct Down {
-  static constexpr uint32_t kStage = stage_bytes(16);
+  static constexpr uint32_t kStage = align128(2 * kSubBytes + 16 * kXRow);
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
   static constexpr uint32_t kBars = kLists + kWarps * kListCap * 4;
@@ -295,7 +319,7 @@ struct Down {
 };
 static_assert(sizeof(RouteScratch) <= Down::kRoute, "scratch");
 
-__global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constant__ Params p,
                                                             const __grid_constant__ Planes planes, uint32_t csize) {
   extern __shared__ __align__(128) uint8_t dyn[];
   Route &r = *reinterpret_cast<Route *>(dyn + Down::kRoute);
@@ -315,59 +339,61 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
   const uint32_t q0 = ok ? uint32_t(uint64_t(all) * rank / csize) : 0u, q1 = ok ? uint32_t(uint64_t(all) * (rank + 1) / csize) : 0u;
   const uint32_t first = q0 / per, st0 = q0 - first * per;  // item, stage of it
   if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
+  Turn turn;
   if (warp == kWarps) {
     fence_async();  // the routing's scratch was in the ring
     const uint64_t plane = uint64_t(p.T) * p.k * p.F;
-    uint32_t item = first, st = st0;
+    struct At {
+      uint32_t item, st;
+    } at{first, st0};
+    auto step = [&](At &a) {
+      if (++a.st == per) {
+        a.st = 0;
+        a.item++;
+      }
+    };
     auto subs_of = [&](uint32_t st) { return 2 * st + 1 < units ? 2u : 1u; };
-    auto weights = [&](uint32_t s, uint32_t item, uint32_t st) {
-      uint64_t *full = &bars.full[s % kDepth];
-      const uint32_t slot = ring + s % kDepth * Down::kStage, subs = subs_of(st);
-      const uint32_t row = uint32_t(r.item_e[item]) * p.H + n0;
+    auto weights = [&](const Turn &turn, const At &a) {
+      uint64_t *full = &bars.full[turn.slot];
+      const uint32_t slot = ring + turn.slot * Down::kStage, subs = subs_of(a.st);
+      const uint32_t row = uint32_t(r.item_e[a.item]) * p.H + n0;
       if (lane == 0) {
-        bar_expect(full, subs * (kSubBytes + r.item_n[item] * 4 * kUnit));
-        for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (2 * st + i) * kUnit, row, full);
+        bar_expect(full, subs * (kSubBytes + r.item_n[a.item] * 4 * kUnit));
+        for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (2 * a.st + i) * kUnit, row, full);
       }
       __syncwarp();
     };
-    auto values = [&](uint32_t s, uint32_t item, uint32_t st) {  // lanes 0-7: the first plane, 8-15: the second
+    auto values = [&](const Turn &turn, const At &a) {  // lanes 0-7: the first plane, 8-15: the second
       const uint32_t i = lane & 7;
-      if (lane < 16 && i < r.item_n[item])
-        load_row(ring + s % kDepth * Down::kStage + 2 * kSubBytes + lane * kXRow,
-                 p.hs + (lane >> 3) * plane + uint64_t(r.pair[r.item_first[item] + i]) * K + 2 * st * kUnit,
-                 subs_of(st) * 2 * kUnit, &bars.full[s % kDepth]);
-    };
-    auto step = [&] {
-      if (++st == per) {
-        st = 0;
-        item++;
-      }
+      if (lane < 16 && i < r.item_n[a.item])
+        load_row(ring + turn.slot * Down::kStage + 2 * kSubBytes + lane * kXRow,
+                 p.hs + (lane >> 3) * plane + uint64_t(r.pair[r.item_first[a.item] + i]) * K + 2 * a.st * kUnit,
+                 subs_of(a.st) * 2 * kUnit, &bars.full[turn.slot]);
     };
     // the weights of the first stages are on their way before hs is waited
     // for, its values follow
     uint32_t s = 0;
-    for (uint32_t q = q0; q < q1 && s < kDepth; q++, s++) {
-      weights(s, item, st);
-      step();
+    for (; q0 + s < q1 && s < kDepth; s++, turn.next()) {
+      weights(turn, at);
+      step(at);
     }
     wait_prerequisites();
     asm volatile("fence.proxy.async.global;" ::: "memory");
-    item = first;
-    st = st0;
-    for (uint32_t i = 0; i < s; i++) {
-      values(i, item, st);
-      step();
+    Turn turn2;
+    At at2{first, st0};
+    for (uint32_t i = 0; i < s; i++, turn2.next()) {
+      values(turn2, at2);
+      step(at2);
     }
-    for (uint32_t q = q0 + s; q < q1; q++, s++) {
-      if (!bar_wait(bars, &bars.empty[s % kDepth], (s / kDepth - 1) & 1u, true, p.status)) break;
-      weights(s, item, st);
-      values(s, item, st);
-      step();
+    for (; q0 + s < q1; s++, turn.next()) {
+      if (!bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) break;
+      weights(turn, at);
+      values(turn, at);
+      step(at);
     }
-    // no copy is in flight when the CTA ends
-    for (uint32_t i = s > kDepth ? s - kDepth : 0; i < s; i++) bar_wait(bars, &bars.full[i % kDepth], (i / kDepth) & 1u, false, p.status);
+    finish_copies(bars, turn, s, p.status);
   } else if (q0 < q1) {
-    const uint32_t group = warp & 3, sub = warp >> 2, row0 = n0 + kRows * group, last = (q1 - 1) / per;
+    const uint32_t row0 = n0 + kRows * warp, last = (q1 - 1) / per;
     auto row_of = [&](uint32_t item) { return uint64_t(r.item_e[item]) * p.H + row0; };
     Window now, next;
     auto offsets = [&](Window &w, uint32_t i) {
@@ -381,28 +407,34 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
     entries(now, first);
     Exceptions x;
     x.list = reinterpret_cast<uint32_t *>(dyn + Down::kLists) + warp * kListCap;
-    uint32_t s = 0, st = st0;
+    const XAt xat = x_rows(lane);
+    uint32_t st = st0;
     bool alive = true;
     for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
       const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
       exceptions_reset(x);
       if (v.ne > 0) {
-        window_keep(x, now, v, row_of(item), K, 2 * st + sub, 2 * end, 2, lane, p.status);
-        exceptions_ready(x, lane);
+        window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
+        exceptions_ready(x, 2 * st, lane);
       }
       now = next;
       entries(now, item + 1);
       offsets(next, item + 2);
-      float tot[1][4] = {};
-      for (; st < end; st++, q++, s++) {
-        alive = bar_wait(bars, &bars.full[s % kDepth], (s / kDepth) & 1u, true, p.status);
+      float tot0[1][4] = {}, tot1[1][4] = {};
+      for (; st < end; st++, q++, turn.next()) {
+        alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
         if (!alive) break;
-        const uint32_t slot = ring + s % kDepth * Down::kStage, at = slot + sub * kSubBytes, u = 2 * st + sub;
-        if (u < units)
-          unit_product<1, 2>(tot, at + group * kRows * 32, at + kIdxBytes + group * kRows * 64,
-                             slot + 2 * kSubBytes + sub * 2 * kUnit, v.book, v, x, u, row_of(item) + (lane >> 2), K, lane);
+        const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
+        if (u + 1 < units && x.next > u + 1) {
+          stage_product<1, 2, false>(tot0, tot1, slot, warp, xs, xs + 2 * kUnit, xat, 8 * kXRow, v.book, lane);
+        } else {
+#pragma unroll 1
+          for (uint32_t i = 0; i < 2 && u + i < units; i++)
+            subtile_product<1, 2>(tot0, slot + i * kSubBytes, warp, xs + i * 2 * kUnit, xat, 8 * kXRow, v, x, u + i, u + i,
+                                  row_of(item) + (lane >> 2), K, lane);
+        }
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.empty[s % kDepth]);
+        if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
       // columns to tokens; a token that did not choose the expert gets
       // nothing (not even zero times an infinite weight)
@@ -411,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
       for (uint32_t i = 0; i < 2; i++)
         if (2 * t + i < n) {
           float *to = acc + r.pair[from + 2 * t + i] / p.k * kRedTok + g;
-          to[0] += tot[0][i];
-          to[8] += tot[0][2 + i];
+          to[0] += tot0[0][i] + tot1[0][i];
+          to[8] += tot0[0][2 + i] + tot1[0][2 + i];
         }
     }
   }
@@ -424,10 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
       const uint32_t row = o % kSubRows, m = o / kSubRows;
       const float *from = sums + (row / kRows * p.T + m) * kRedTok + row % kRows;
       float sum = 0.0f;
-      for (uint32_t c = 0; c < csize; c++) {
-        if (csize > 1) sum += cluster_load(from, c) + cluster_load(from + 4 * p.T * kRedTok, c);
-        else sum = from[0] + from[4 * p.T * kRedTok];
-      }
+      for (uint32_t c = 0; c < csize; c++) sum += csize > 1 ? cluster_load(from, c) : *from;
       const uint64_t at = uint64_t(m) * p.H + n0 + row;
       if (p.wide) static_cast<float *>(p.out)[at] = sum;
       else static_cast<uint16_t *>(p.out)[at] = uint16_t(bf16_bits(sum));
@@ -490,11 +519,11 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     p.x = static_cast<const uint16_t *>(d_x) + uint64_t(m) * H;
     p.logits = d_logits + uint64_t(m) * E;
     p.out = static_cast<uint8_t *>(d_out) + uint64_t(m) * H * (p.wide ? 4 : 2);
-    // up: clusters that split H until about 3 CTAs an SM have work; with
+    // up: clusters that split H until about 4 CTAs an SM have work; with
     // more jobs than that, as many CTAs as run at once
     const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows), slots = uint32_t(sms * up_per_sm);
     uint32_t cu = 1;
-    while (cu < 8 && jobs * cu * 2 <= 3u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
+    while (cu < 8 && jobs * cu * 2 <= 4u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
     // down: CTAs that split the items, the same
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
     uint32_t cd = 1;

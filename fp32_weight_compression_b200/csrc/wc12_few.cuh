@@ -16,19 +16,13 @@
 // token (column g) as 32 bytes.  Four products (steps) use them up, 4 values
 // of a lane's row each.
 //
-// Loads.  A stage is two subtiles of 64 rows x 64 values of K, each the work
-// of 4 warps (16 rows each): two ranges of rows with the same values of K, or
-// the same rows with two successive ranges.  One warp brings the subtiles'
-// planes with TMA and the tokens' values with bulk copies, a row each, into a
-// ring of kDepth stages; 8 warps expand and multiply.  No barrier of the CTA
-// in the loop: a "full" and an "empty" mbarrier a stage.  The planes' boxes
-// are stored as rows of 32 and 64 bytes, so that the lanes that read together
-// read 128 bytes in a row; the tokens' rows are 272 bytes apart for the same
-// reason.  (First with loads to registers, 8-byte and 16-byte ones, two
-// stages ahead: 25 us for a 4096 x 4096 layer and one token, the tokens'
-// values being fetched from L2 at the moment of use.  Then with the same
-// pieces copied ahead by cp.async: 13 us; 56 us for 14336 x 4096 and 16
-// tokens, twice the instructions of the product itself.)
+// Loads.  A stage is two subtiles of 64 rows x 64 values of K, 16 rows of
+// each the work of a warp: two successive ranges of K, or two matrices' rows
+// with the same values of K.  One warp brings the subtiles' planes with TMA
+// and the tokens' values into a ring of kDepth stages, four warps expand and
+// multiply.  No barrier of the CTA in the loop: a "full" and an "empty"
+// mbarrier a stage.  The planes' boxes are stored as rows of 32 and 64 bytes,
+// so that the lanes that read together read 128 bytes in a row.
 //
 // Every wait is bounded and gives up once another thread has; the kernel then
 // reports WC_ERR_TIMEOUT, waits for its copies in flight and ends.
@@ -39,7 +33,9 @@
 // container's per-chunk lists, 64 entries a load, while its first weights are
 // in flight (or the ones of the rows before), and keeps those of its part of
 // K, one a lane.  More than its list holds: it looks each lane's values up in
-// the container's sorted lists instead (slow, and right for any container).
+// the container's sorted lists instead (slow, and right for any container).  A
+// stage without exceptions, which most are, is multiplied by code without a
+// branch.
 #pragma once
 
 #include <cstdint>
@@ -61,7 +57,7 @@ namespace wc12f {
 
 using wc12::kChunk;
 
-constexpr int kWarps = 8;                   // that multiply
+constexpr int kWarps = 4;                   // that multiply
 constexpr int kConsumers = 32 * kWarps;
 constexpr int kThreads = kConsumers + 32;   // and one that loads
 constexpr uint32_t kRows = 16;       // weight rows of a group
@@ -70,7 +66,7 @@ constexpr uint32_t kUnit = 64;       // values of K of a subtile
 constexpr uint32_t kMaxK = 1 << 16;  // a group's rows touch at most 17 chunks
 constexpr uint32_t kListCap = 256;   // exceptions a warp keeps
 constexpr uint32_t kRedTok = 18;     // floats a token's 16 sums take (padded: few bank conflicts)
-constexpr uint32_t kDepth = 4;       // stages of the ring
+constexpr uint32_t kDepth = 3;       // stages of the ring
 constexpr uint32_t kSpinLimit = 1u << 24;
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
@@ -153,9 +149,24 @@ __device__ __forceinline__ bool open_header(View &v, const uint8_t *w, uint64_t 
 // The ring.
 constexpr uint32_t kIdxBytes = kSubRows * kUnit / 2, kLoBytes = kSubRows * kUnit;
 constexpr uint32_t kSubBytes = kIdxBytes + kLoBytes;
-constexpr uint32_t kXRow = 272;  // bytes from one token's values to the next one's
-// a stage with n rows of tokens' values, whose place it starts at 2 kSubBytes
-__host__ __device__ constexpr uint32_t stage_bytes(uint32_t n) { return (2 * kSubBytes + n * kXRow + 127) / 128 * 128; }
+// The tokens' values of a stage, from 2 kSubBytes on, as the lanes read them:
+// from the start of the stage's values to this lane's token's (the first of
+// each 8), its first and second 8 of the 16 values of a unit.  Copied a row
+// at a time: kXRow bytes a token (so that 8 lanes read from all banks), the
+// second unit's values behind the first's.  By TMA: a box of 8 kTiles rows of
+// 128 bytes a unit, 128-byte swizzle.
+struct XAt {
+  uint32_t first, second;
+};
+constexpr uint32_t kXRow = 272;
+__device__ __forceinline__ XAt x_rows(uint32_t lane) {
+  const uint32_t at = (lane >> 2) * kXRow + 32 * (lane & 3);
+  return {at, at + 16};
+}
+__device__ __forceinline__ XAt x_boxes(uint32_t lane) {
+  const uint32_t g = lane >> 2, t = lane & 3;
+  return {128 * g + (((2 * t) ^ g) << 4), 128 * g + (((2 * t + 1) ^ g) << 4)};
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint4 shared16(uint32_t a) {
@@ -185,11 +196,20 @@ __device__ __forceinline__ void bars_init(Bars &b) {
   b.failed = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
+// A place in the ring: stage s is in slot s % kDepth, its turn s / kDepth.
+struct Turn {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kDepth) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
 // whether the phase of the given parity came to its end, for the whole warp
 __device__ __forceinline__ bool bar_wait(Bars &b, uint64_t *bar, uint32_t parity, bool heed_failure, int32_t *status) {
   const uint32_t a = smem_u32(bar);
-  bool done = false;
-  for (uint32_t i = 0; i < kSpinLimit && !done; i++) {
+  auto look = [&] {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -198,13 +218,30 @@ __device__ __forceinline__ bool bar_wait(Bars &b, uint64_t *bar, uint32_t parity
         : "=r"(r)
         : "r"(a), "r"(parity)
         : "memory");
-    done = r != 0;
-    if (!done && heed_failure && *static_cast<volatile int *>(&b.failed)) break;
+    return __all_sync(0xffffffffu, r != 0);
+  };
+  if (look()) return true;
+  for (uint32_t i = 0; i < kSpinLimit; i++) {
+    if (look()) return true;
+    if (heed_failure && __any_sync(0xffffffffu, *static_cast<volatile int *>(&b.failed) != 0)) return false;
   }
-  if (__all_sync(0xffffffffu, done)) return true;
-  if (!*static_cast<volatile int *>(&b.failed)) report(status, WC_ERR_TIMEOUT);
+  report(status, WC_ERR_TIMEOUT);
   *static_cast<volatile int *>(&b.failed) = 1;
   return false;
+}
+// the loading warp, before it ends: no copy may be in flight then.  turn: the
+// place after the last of `count` stages
+__device__ __forceinline__ void finish_copies(Bars &b, Turn turn, uint32_t count, int32_t *status) {
+  // back to the first of the last kDepth stages (or of all)
+  const uint32_t n = count < kDepth ? count : kDepth;
+  for (uint32_t i = 0; i < n; i++) {
+    if (turn.slot == 0) {
+      turn.slot = kDepth;
+      turn.parity ^= 1;
+    }
+    turn.slot--;
+  }
+  for (uint32_t i = 0; i < n; i++, turn.next()) bar_wait(b, &b.full[turn.slot], turn.parity, false, status);
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
@@ -235,9 +272,6 @@ __device__ __forceinline__ void load_subtile(uint32_t dst, const Planes &m, uint
   load_box(dst, &m.idx, k / 2, row, bar);
   load_box(dst + kIdxBytes, &m.lo, k, row, bar);
 }
-// all 8 multiplying warps
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
-
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
@@ -264,10 +298,12 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
 
 // ---------------------------------------------------------------------------
 // Exceptions.  An entry: high byte (bits 0-7), row of the group (8-11),
-// column of the unit (12-17), unit of the row (18-31).
-constexpr uint32_t kExcUnit = 18;
-__device__ __forceinline__ uint32_t pack_exc(uint32_t unit, uint32_t col, uint32_t row, uint32_t high) {
-  return high | (row << 8) | (col << 12) | (unit << kExcUnit);
+// column of the unit (12-17), key (18-31): which subtile of the warp's rows,
+// numbered as the warp meets them.
+constexpr uint32_t kExcKey = 18;
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t pack_exc(uint32_t key, uint32_t col, uint32_t row, uint32_t high) {
+  return high | (row << 8) | (col << 12) | (key << kExcKey);
 }
 __device__ __forceinline__ uint32_t exc_step(uint32_t e) { return (e >> 14) & 3u; }  // the product that uses it
 // puts the entry's high byte into the A words of its step, in its lane
@@ -311,16 +347,17 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
 }
 
 // What a warp keeps of its exceptions: cnt entries in `list`, the lane's one
-// of the first 32 in e; walk: too many, look them up.
+// of the first 32 in e, the next subtile that has any in `next`; walk: too
+// many, look them up.
 struct Exceptions {
   uint32_t *list;
-  uint32_t cnt, e;
+  uint32_t cnt, e, next;
   bool walk;
 };
-// Entries have come: keeps those of the group's units u0, u0 + step .. (below
-// u1); step 1 or 2.
+// Entries have come: keeps those of the group's units [u0, u1), as of
+// subtile mul * unit + plus.
 __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, const View &v, uint64_t row0, uint32_t K,
-                                            uint32_t u0, uint32_t u1, uint32_t step, uint32_t lane, int32_t *status) {
+                                            uint32_t u0, uint32_t u1, uint32_t mul, uint32_t plus, uint32_t lane, int32_t *status) {
   const uint64_t e0 = __shfl_sync(0xffffffffu, w.off, 0), e1 = __shfl_sync(0xffffffffu, w.off, 31);
   const uint64_t before = __shfl_up_sync(0xffffffffu, w.off, 1);
   if (__any_sync(0xffffffffu, (lane > 0 && w.off < before) || w.off > v.ne)) {
@@ -345,26 +382,43 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
       if (in && f >= v.n) report(status, WC_ERR_CORRUPT);
       in = in && f >= f0 && f - f0 < uint64_t(kRows) * K;
       const uint32_t lf = in ? uint32_t(f - f0) : 0u, row = lf / K, col = lf - row * K, u = col / kUnit;
-      in = in && u >= u0 && u < u1 && ((u - u0) & (step - 1)) == 0;
+      in = in && u >= u0 && u < u1;
       const uint32_t m = __ballot_sync(0xffffffffu, in);
       if (x.cnt + __popc(m) > kListCap) {
         x.walk = true;
         return;
       }
-      if (in) x.list[x.cnt + __popc(m & ((1u << lane) - 1u))] = pack_exc(u, col % kUnit, row, (val >> (8 * i)) & 0xFFu);
+      if (in) x.list[x.cnt + __popc(m & ((1u << lane) - 1u))] = pack_exc(mul * u + plus, col % kUnit, row, (val >> (8 * i)) & 0xFFu);
       x.cnt += __popc(m);
     }
   }
 }
+// the first subtile from `key` on that has an exception
+__device__ __forceinline__ void exceptions_seek(Exceptions &x, uint32_t key, uint32_t lane) {
+  if (x.walk) {
+    x.next = key;
+    return;
+  }
+  x.next = kNoKey;
+  if (x.cnt == 0) return;
+  uint32_t own = lane < x.cnt && (x.e >> kExcKey) >= key ? x.e >> kExcKey : kNoKey;
+  for (uint32_t i = 32 + lane; i < x.cnt; i += 32) {
+    const uint32_t k = x.list[i] >> kExcKey;
+    if (k >= key && k < own) own = k;
+  }
+  x.next = __reduce_min_sync(0xffffffffu, own);
+}
 __device__ __forceinline__ void exceptions_reset(Exceptions &x) {
   x.cnt = 0;
   x.e = 0;
+  x.next = kNoKey;
   x.walk = false;
   __syncwarp();  // the list may be written again
 }
-__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
+__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t key, uint32_t lane) {
   __syncwarp();
   x.e = lane < x.cnt ? x.list[lane] : 0u;
+  exceptions_seek(x, key, lane);
 }
 
 // Replaces the high bytes of a lane's words of a step by the exceptions that
@@ -400,84 +454,139 @@ __device__ __forceinline__ void walk_patch(uint32_t *a, const View &v, uint64_t 
   }
 }
 
-// A warp's 16 rows of a subtile times 8 kTiles tokens, added to tot.  sub: its
-// rows' start in the subtile's index plane; xs: the tokens' values, kParts
-// rows of 8 kTiles tokens each (a value held as the sum of kParts bf16
-// numbers).  The four products of a unit are added up in the tensor cores,
-// units in fp32 registers: the tensor cores cut off what their accumulator
-// cannot hold, so that long sums there drift toward zero.  Columns without a
-// token hold sums that the caller drops.  row_g: the lane's first row.
-template <int kTiles, int kParts>
-__device__ __forceinline__ void unit_product(float tot[kTiles][4], uint32_t idx_at, uint32_t lo_at, uint32_t xs, uint4 book,
-                                             const View &v, const Exceptions &x, uint32_t unit, uint64_t row_g,
-                                             uint32_t K, uint32_t lane) {
-  const uint32_t g = lane >> 2, t = lane & 3;
+// the same with a zero accumulator
+__device__ __forceinline__ void mma_first(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// A lane's 16 values of two rows of a subtile, as stored.
+struct Piece {
   uint2 idx[2];
-  uint4 lo[2], xv[kTiles][kParts];
+  uint4 lo[2];
+};
+// sub: the subtile's start, group: which 16 rows
+__device__ __forceinline__ void read_piece(Piece &f, uint32_t sub, uint32_t group, uint32_t lane) {
+  const uint32_t g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; h++) {
-    idx[h] = shared8(idx_at + (g + 8 * h) * 32 + 8 * t);
-    lo[h] = shared16(lo_at + (g + 8 * h) * 64 + 16 * t);
+    f.idx[h] = shared8(sub + (group * kRows + g + 8 * h) * 32 + 8 * t);
+    f.lo[h] = shared16(sub + kIdxBytes + (group * kRows + g + 8 * h) * 64 + 16 * t);
   }
-  float d[kTiles][4];
+}
+// the A fragment of step s (a constant once unrolled)
+__device__ __forceinline__ void expand_step(uint32_t *a, const Piece &f, int s, uint4 book) {
 #pragma unroll
-  for (int i = 0; i < kTiles; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
-  // the unit's exceptions: lanes that hold one, steps that have one
-  uint32_t hit = 0, steps = 0;
-  if (x.walk) {
-    steps = 0xFu;
-  } else if (x.cnt > 32) {
-    steps = 0xFu;
-  } else if (x.cnt > 0) {
-    const bool mine = lane < x.cnt && (x.e >> kExcUnit) == unit;
-    hit = __ballot_sync(0xffffffffu, mine);
-    if (hit) steps = __reduce_or_sync(0xffffffffu, mine ? 1u << exc_step(x.e) : 0u);
+  for (int h = 0; h < 2; h++) {
+    const uint32_t qw = s < 2 ? f.idx[h].x : f.idx[h].y;
+    const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
+    const uint32_t lw = s == 0 ? f.lo[h].x : s == 1 ? f.lo[h].y : s == 2 ? f.lo[h].z : f.lo[h].w;
+    const uint2 e = expand4(sel, up, book, lw);
+    a[h] = e.x;
+    a[h + 2] = e.y;
   }
+}
+// step s with kParts planes of kTiles x 8 tokens
+template <int kTiles, int kParts>
+__device__ __forceinline__ void multiply_step(float d[kTiles][4], const uint32_t *a, const uint4 xv[kTiles][kParts], int s) {
+#pragma unroll
+  for (int i = 0; i < kTiles; i++)
+#pragma unroll
+    for (int part = 0; part < kParts; part++) {
+      const uint4 q = xv[i][part];
+      if (s == 0 && part == 0) mma_first(d[i], a, q.x, q.y);
+      else mma(d[i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
+    }
+}
+template <int kTiles, int kParts>
+__device__ __forceinline__ void read_values(uint4 xv[kTiles][kParts], uint32_t at, uint32_t tile_bytes) {
+#pragma unroll
+  for (int i = 0; i < kTiles; i++)
+#pragma unroll
+    for (int part = 0; part < kParts; part++) xv[i][part] = shared16(at + (part * kTiles + i) * tile_bytes);
+}
+
+// A warp's 16 rows of both subtiles of a stage times 8 kTiles tokens, added to
+// tot[0] and tot[1].  xs, xs2: where the tokens' values of either subtile
+// start (the same place for two matrices: kShare); tile_bytes: from 8 tokens
+// to the next 8 (then the next plane: a value is held as the sum of kParts
+// bf16 numbers).  The four products of a subtile are added up in the tensor
+// cores, subtiles in fp32 registers: the tensor cores cut off what their
+// accumulator cannot hold, so that long sums there drift toward zero.
+// Columns without a token hold sums that the caller drops.
+template <int kTiles, int kParts, bool kShare>
+__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], uint32_t slot, uint32_t group,
+                                              uint32_t xs, uint32_t xs2, XAt xat, uint32_t tile_bytes, uint4 book,
+                                              uint32_t lane) {
+  Piece f0, f1;
+  read_piece(f0, slot, group, lane);
+  read_piece(f1, slot + kSubBytes, group, lane);
+  float d0[kTiles][4], d1[kTiles][4];
+  uint4 xv[kTiles][kParts], xw[kTiles][kParts];
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     if ((s & 1) == 0) {  // 8 values of each token, for two steps
-#pragma unroll
-      for (int i = 0; i < kTiles; i++)
-#pragma unroll
-        for (int part = 0; part < kParts; part++)
-          xv[i][part] = shared16(xs + ((part * kTiles + i) * 8 + g) * kXRow + 32 * t + 8 * s);
+      read_values<kTiles, kParts>(xv, xs + (s ? xat.second : xat.first), tile_bytes);
+      if (!kShare) read_values<kTiles, kParts>(xw, xs2 + (s ? xat.second : xat.first), tile_bytes);
     }
+    uint32_t a[4], b[4];
+    expand_step(a, f0, s, book);
+    multiply_step<kTiles, kParts>(d0, a, xv, s);
+    expand_step(b, f1, s, book);
+    multiply_step<kTiles, kParts>(d1, b, kShare ? xv : xw, s);
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      tot0[i][j] += d0[i][j];
+      tot1[i][j] += d1[i][j];
+    }
+}
+
+// One subtile, the one of exceptions x.next's key or any other; unit: which of
+// the row's, row_g: the lane's first row.
+template <int kTiles, int kParts>
+__device__ __forceinline__ void subtile_product(float tot[kTiles][4], uint32_t sub, uint32_t group, uint32_t xs, XAt xat,
+                                                uint32_t tile_bytes, const View &v, Exceptions &x, uint32_t key,
+                                                uint32_t unit, uint64_t row_g, uint32_t K, uint32_t lane) {
+  Piece f;
+  read_piece(f, sub, group, lane);
+  const bool any = key == x.next;
+  uint32_t hit = 0;  // lanes whose one is of this subtile
+  if (any && !x.walk) hit = __ballot_sync(0xffffffffu, lane < x.cnt && (x.e >> kExcKey) == key);
+  float d[kTiles][4];
+  uint4 xv[kTiles][kParts];
+#pragma unroll
+  for (int s = 0; s < 4; s++) {
+    if ((s & 1) == 0) read_values<kTiles, kParts>(xv, xs + (s ? xat.second : xat.first), tile_bytes);
     uint32_t a[4];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const uint32_t qw = s < 2 ? idx[h].x : idx[h].y;
-      const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
-      const uint32_t lw = s == 0 ? lo[h].x : s == 1 ? lo[h].y : s == 2 ? lo[h].z : lo[h].w;
-      const uint2 e = expand4(sel, up, book, lw);
-      a[h] = e.x;
-      a[h + 2] = e.y;
-    }
-    if ((steps >> s) & 1u) {
+    expand_step(a, f, s, v.book);
+    if (any) {
       if (x.walk) {
-        walk_patch(a, v, row_g * K + kUnit * unit + 16 * t + 4 * s, K);
-      } else if (x.cnt > 32) {
-        for (uint32_t i = 0; i < x.cnt; i += 32) {
-          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
-          uint32_t rest = __ballot_sync(0xffffffffu, i + lane < x.cnt && (own >> kExcUnit) == unit && exc_step(own) == uint32_t(s));
-          for (; rest; rest &= rest - 1) patch(a, __shfl_sync(0xffffffffu, own, __ffs(rest) - 1), lane);
-        }
+        walk_patch(a, v, row_g * K + kUnit * unit + 16 * (lane & 3u) + 4 * s, K);
       } else {
         for (uint32_t rest = hit; rest; rest &= rest - 1) {
           const uint32_t e = __shfl_sync(0xffffffffu, x.e, __ffs(rest) - 1);
           if (exc_step(e) == uint32_t(s)) patch(a, e, lane);
         }
+        for (uint32_t i = 32; i < x.cnt; i += 32) {
+          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
+          uint32_t rest = __ballot_sync(0xffffffffu, i + lane < x.cnt && (own >> kExcKey) == key && exc_step(own) == uint32_t(s));
+          for (; rest; rest &= rest - 1) patch(a, __shfl_sync(0xffffffffu, own, __ffs(rest) - 1), lane);
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < kTiles; i++)
-#pragma unroll
-      for (int part = 0; part < kParts; part++)
-        mma(d[i], a, s & 1 ? xv[i][part].z : xv[i][part].x, s & 1 ? xv[i][part].w : xv[i][part].y);
+    multiply_step<kTiles, kParts>(d, a, xv, s);
   }
 #pragma unroll
   for (int i = 0; i < kTiles; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++) tot[i][j] += d[i][j];
+  if (any) exceptions_seek(x, key + 1, lane);
 }
 
 // A warp's sums of a group, [token][row] with kRedTok floats a token.
