@@ -196,21 +196,15 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
       if (v.ne > 0) {
         window_entries(win, v, lane);
         window_keep(x, win, v, row0, K, u0, u1, 1, 0, lane, p.status);
-        exceptions_ready(x, u0, lane);
+        exceptions_ready(x, lane);
       }
       const XAt xat = x_boxes(lane);
       Turn turn;
       for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
         const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
-        if (u + 1 < u1 && x.next > u + 1) {
-          stage_product<NT, 1, false>(tot0, tot1, slot, warp, xs, xs + F::kXBox, xat, 1024, v.book, lane);
-        } else {
-#pragma unroll 1
-          for (uint32_t i = 0; i < 2 && u + i < u1; i++)
-            subtile_product<NT, 1>(tot0, slot + i * kSubBytes, warp, xs + i * F::kXBox, xat, 1024, v, x, u + i, u + i,
-                                   row0 + (lane >> 2), K, lane);
-        }
+        stage_product<NT, 1, false>(tot0, tot1, {slot, warp, xs, xs + F::kXBox, 1024, u}, xat, u + 1 == u1, v, x, u, u + 1, row0,
+                                    row0, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

@@ -61,7 +61,7 @@ struct Route {
 };
 // while it is found (in shared memory that the ring takes later)
 struct RouteScratch {
-  uint32_t key[kThreads / 32][kMaxExperts];
+  uint32_t key[8192];           // of as many tokens as fit
   uint32_t who[kMaxExperts];    // the tokens that chose each expert, a bit each
   uint16_t first[kMaxExperts];  // their first place in pair[]
 };
@@ -73,48 +73,58 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_key(-inf)
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
 __device__ void route(Route &r, RouteScratch &w, const Params &p) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (uint32_t e = tid; e < p.E; e += kThreads) w.who[e] = 0;
-  __syncthreads();
-  for (uint32_t m = warp; m < p.T; m += kThreads / 32) {
-    const float *l = p.logits + uint64_t(m) * p.E;
-    uint32_t *key = w.key[warp];
-    // each lane looks at its own experts only: no barrier needed
-    for (uint32_t e = lane; e < p.E; e += 32) key[e] = order_key(l[e]);
-    uint32_t taken = 0;  // of the lane's experts
-    float top = 0.0f, sum = 0.0f, ex = 0.0f;
-    for (uint32_t j = 0; j < p.k; j++) {
-      uint32_t best = 0, at = 0xFFFFFFFFu;
-      for (uint32_t i = 0, e = lane; e < p.E; i++, e += 32)
-        if (!((taken >> i) & 1u) && key[e] > best) {
-          best = key[e];
-          at = e;
+  const uint32_t batch = 8192 / p.E;
+  for (uint32_t m0 = 0; m0 < p.T; m0 += batch) {
+    const uint32_t some = p.T - m0 < batch ? p.T - m0 : batch;
+#pragma unroll 4
+    for (uint32_t i = tid; i < some * p.E; i += kThreads) w.key[i] = order_key(p.logits[uint64_t(m0) * p.E + i]);
+    __syncthreads();
+    for (uint32_t m = m0 + warp; m < m0 + some; m += kThreads / 32) {
+      const uint32_t *key = w.key + (m - m0) * p.E;
+      uint32_t taken = 0;               // of the lane's experts
+      uint32_t mine = 0, mine_e = 0;    // lane j: the j-th largest key and its expert
+      uint32_t top = 0;
+      for (uint32_t j = 0; j < p.k; j++) {
+        uint32_t best = 0, at = 0xFFFFFFFFu;
+        for (uint32_t i = 0, e = lane; e < p.E; i++, e += 32) {
+          const uint32_t q = key[e];
+          if (!((taken >> i) & 1u) && q > best) {
+            best = q;
+            at = e;
+          }
         }
-      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? at : 0xFFFFFFFFu);
-      const bool none = high <= kMinusInf;  // only -inf is left
-      if (!none) {
+        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? at : 0xFFFFFFFFu);
+        if (high <= kMinusInf) break;  // only -inf is left
         if ((e & 31u) == lane) taken |= 1u << (e >> 5);
-        const float v = l[e];
-        if (j == 0) top = v;
-        const float q = expf(v - top);
-        if (lane == j) ex = q;
-        sum += q;
-        if (lane == 0) atomicOr(&w.who[e], 1u << m);
+        if (lane == j) {
+          mine = high;
+          mine_e = e;
+        }
+        if (j == 0) top = high;
       }
-      if (lane == 0) r.id[m][j] = none ? int16_t(-1) : int16_t(e);
-    }
-    if (!p.renormalize) {
-      sum = 0.0f;
-      for (uint32_t e = lane; e < p.E; e += 32) sum += expf(l[e] - top);
+      const float largest = key_value(top);
+      const float ex = mine != 0 ? expf(key_value(mine) - largest) : 0.0f;
+      float sum = ex;
+      if (!p.renormalize) {
+        sum = 0.0f;
+        for (uint32_t e = lane; e < p.E; e += 32) sum += expf(key_value(key[e]) - largest);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < p.k) {
+        r.id[m][lane] = mine != 0 ? int16_t(mine_e) : int16_t(-1);
+        r.p[m][lane] = ex / sum;
+        if (mine != 0) atomicOr(&w.who[mine_e], 1u << m);
+      }
     }
-    if (lane < p.k) r.p[m][lane] = ex / sum;
+    __syncthreads();
   }
-  __syncthreads();
   // the experts' places in pair[], and their items
   if (warp == 0) {
     uint32_t pairs = 0, items = 0;
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
     if (v.ne > 0) {
 #pragma unroll 1
       for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
-      exceptions_ready(x, 2 * u0, lane);
+      exceptions_ready(x, lane);
     }
     now[0] = next[0];
     now[1] = next[1];
@@ -267,12 +277,8 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
       alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
-      if (x.next > 2 * u + 1) {
-        stage_product<1, 1, true>(gate, up, slot, warp, xs, xs, xat, 0, v.book, lane);
-      } else {
-        subtile_product<1, 1>(gate, slot, warp, xs, xat, 0, v, x, 2 * u, u, row_of(job, 0) + g, K, lane);
-        subtile_product<1, 1>(up, slot + kSubBytes, warp, xs, xat, 0, v, x, 2 * u + 1, u, row_of(job, 1) + g, K, lane);
-      }
+      stage_product<1, 1, true>(gate, up, {slot, warp, xs, xs, 0, 2 * u}, xat, false, v, x, u, u, row_of(job, 0), row_of(job, 1), K,
+                                lane);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       exceptions_reset(x);
       if (v.ne > 0) {
         window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
-        exceptions_ready(x, 2 * st, lane);
+        exceptions_ready(x, lane);
       }
       now = next;
       entries(now, item + 1);
@@ -425,14 +431,8 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
         alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
         if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
-        if (u + 1 < units && x.next > u + 1) {
-          stage_product<1, 2, false>(tot0, tot1, slot, warp, xs, xs + 2 * kUnit, xat, 8 * kXRow, v.book, lane);
-        } else {
-#pragma unroll 1
-          for (uint32_t i = 0; i < 2 && u + i < units; i++)
-            subtile_product<1, 2>(tot0, slot + i * kSubBytes, warp, xs + i * 2 * kUnit, xat, 8 * kXRow, v, x, u + i, u + i,
-                                  row_of(item) + (lane >> 2), K, lane);
-        }
+        stage_product<1, 2, false>(tot0, tot1, {slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u}, xat, u + 1 == units, v, x, u, u + 1,
+                                   row_of(item), row_of(item), K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

@@ -33,9 +33,9 @@
 // container's per-chunk lists, 64 entries a load, while its first weights are
 // in flight (or the ones of the rows before), and keeps those of its part of
 // K, one a lane.  More than its list holds: it looks each lane's values up in
-// the container's sorted lists instead (slow, and right for any container).  A
-// stage without exceptions, which most are, is multiplied by code without a
-// branch.
+// the container's sorted lists instead (slow, and right for any container).  The
+// products are made by code without a branch, but for the steps that have an
+// exception, which are left out there and made by a loop behind it.
 #pragma once
 
 #include <cstdint>
@@ -171,12 +171,22 @@ __device__ __forceinline__ XAt x_boxes(uint32_t lane) {
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint4 shared16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint2 shared8(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t shared4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t shared2(uint32_t a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a));
   return v;
 }
 
@@ -289,11 +299,18 @@ __device__ __forceinline__ uint2 expand4(uint32_t sel, uint32_t up, uint4 book, 
 }
 
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// unless skip (the same for the whole warp)
+__device__ __forceinline__ void mma_unless(uint32_t skip, float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %10, 0;\n\t"
+      "@p mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n\t}"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(skip));
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +318,6 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
 // column of the unit (12-17), key (18-31): which subtile of the warp's rows,
 // numbered as the warp meets them.
 constexpr uint32_t kExcKey = 18;
-constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t pack_exc(uint32_t key, uint32_t col, uint32_t row, uint32_t high) {
   return high | (row << 8) | (col << 12) | (key << kExcKey);
 }
@@ -347,11 +363,10 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
 }
 
 // What a warp keeps of its exceptions: cnt entries in `list`, the lane's one
-// of the first 32 in e, the next subtile that has any in `next`; walk: too
-// many, look them up.
+// of the first 32 in e; walk: too many, look them up.
 struct Exceptions {
   uint32_t *list;
-  uint32_t cnt, e, next;
+  uint32_t cnt, e;
   bool walk;
 };
 // Entries have come: keeps those of the group's units [u0, u1), as of
@@ -366,22 +381,28 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
   }
   if (e1 - e0 > 64 * kListCap) x.walk = true;
   if (x.walk) return;
-  const uint64_t c0 = row0 * K / kChunk, f0 = row0 * K;
-  const uint32_t chunks = window_chunks(row0, K);
-  for (uint64_t base = e0 & ~uint64_t(1); base < e1; base += 64) {
+  const uint64_t f0 = row0 * K, c0 = f0 / kChunk;
+  const uint32_t chunks = window_chunks(row0, K), count = uint32_t(e1 - e0), skew = uint32_t(e0 & 1);
+  const uint32_t rel = uint32_t(w.off - e0);                              // the lane's chunk's first entry
+  const uint32_t begin = uint32_t(f0 - c0 * kChunk), span = kRows * K;    // of the rows, from the first chunk on
+  const uint64_t left = v.n - c0 * kChunk;                                // values from the first chunk on
+  const float inv = 1.0f / float(K);
+  for (uint32_t base = 0; base < count + skew; base += 64) {  // entry base - skew + 2 lane + i
     uint32_t pos = w.pos, val = w.val;
-    if (base > e0) window_pairs(v, base + 2 * lane, e1, pos, val);
+    if (base > 0) window_pairs(v, e0 - skew + base + 2 * lane, e1, pos, val);
 #pragma unroll
     for (uint32_t i = 0; i < 2; i++) {
-      const uint64_t e = base + 2 * lane + i;
-      bool in = e >= e0 && e < e1;
-      uint64_t c = c0;
-      for (uint32_t j = 1; j < chunks; j++) c += e >= __shfl_sync(0xffffffffu, w.off, j) ? 1u : 0u;
-      const uint32_t p = (pos >> (16 * i)) & 0xFFFFu;
-      const uint64_t f = c * kChunk + p;
-      if (in && f >= v.n) report(status, WC_ERR_CORRUPT);
-      in = in && f >= f0 && f - f0 < uint64_t(kRows) * K;
-      const uint32_t lf = in ? uint32_t(f - f0) : 0u, row = lf / K, col = lf - row * K, u = col / kUnit;
+      const uint32_t e = base + 2 * lane + i - skew;  // wraps for the one before the first
+      uint32_t c = 0;
+      for (uint32_t j = 1; j < chunks; j++) c += e >= __shfl_sync(0xffffffffu, rel, j) ? 1u : 0u;
+      const uint32_t f = c * uint32_t(kChunk) + ((pos >> (16 * i)) & 0xFFFFu);
+      bool in = e < count;
+      if (in && f >= left) report(status, WC_ERR_CORRUPT);
+      in = in && f >= begin && f - begin < span;
+      const uint32_t lf = in ? f - begin : 0u;
+      // lf / K: (lf + 1/2) / K is at least 2^-17 away from a whole number, and
+      // off by less than 2^-19
+      const uint32_t row = uint32_t((float(lf) + 0.5f) * inv), col = lf - row * K, u = col / kUnit;
       in = in && u >= u0 && u < u1;
       const uint32_t m = __ballot_sync(0xffffffffu, in);
       if (x.cnt + __popc(m) > kListCap) {
@@ -393,32 +414,27 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
     }
   }
 }
-// the first subtile from `key` on that has an exception
-__device__ __forceinline__ void exceptions_seek(Exceptions &x, uint32_t key, uint32_t lane) {
-  if (x.walk) {
-    x.next = key;
-    return;
-  }
-  x.next = kNoKey;
-  if (x.cnt == 0) return;
-  uint32_t own = lane < x.cnt && (x.e >> kExcKey) >= key ? x.e >> kExcKey : kNoKey;
-  for (uint32_t i = 32 + lane; i < x.cnt; i += 32) {
-    const uint32_t k = x.list[i] >> kExcKey;
-    if (k >= key && k < own) own = k;
-  }
-  x.next = __reduce_min_sync(0xffffffffu, own);
+// the steps of subtiles key (bits 0-3) and key + 1 (4-7) that have one
+__device__ __forceinline__ uint32_t exceptions_steps(const Exceptions &x, uint32_t key, uint32_t lane) {
+  if (x.walk) return 0xFFu;
+  if (x.cnt == 0) return 0;
+  auto bit = [&](uint32_t e) {
+    const uint32_t d = (e >> kExcKey) - key;
+    return d < 2 ? 1u << (4 * d + exc_step(e)) : 0u;
+  };
+  uint32_t b = lane < x.cnt ? bit(x.e) : 0u;
+  for (uint32_t i = 32 + lane; i < x.cnt; i += 32) b |= bit(x.list[i]);
+  return __reduce_or_sync(0xffffffffu, b);
 }
 __device__ __forceinline__ void exceptions_reset(Exceptions &x) {
   x.cnt = 0;
   x.e = 0;
-  x.next = kNoKey;
   x.walk = false;
   __syncwarp();  // the list may be written again
 }
-__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t key, uint32_t lane) {
+__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
   __syncwarp();
   x.e = lane < x.cnt ? x.list[lane] : 0u;
-  exceptions_seek(x, key, lane);
 }
 
 // Replaces the high bytes of a lane's words of a step by the exceptions that
@@ -454,15 +470,6 @@ __device__ __forceinline__ void walk_patch(uint32_t *a, const View &v, uint64_t 
   }
 }
 
-// the same with a zero accumulator
-__device__ __forceinline__ void mma_first(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
 // A lane's 16 values of two rows of a subtile, as stored.
 struct Piece {
   uint2 idx[2];
@@ -489,18 +496,6 @@ __device__ __forceinline__ void expand_step(uint32_t *a, const Piece &f, int s, 
     a[h + 2] = e.y;
   }
 }
-// step s with kParts planes of kTiles x 8 tokens
-template <int kTiles, int kParts>
-__device__ __forceinline__ void multiply_step(float d[kTiles][4], const uint32_t *a, const uint4 xv[kTiles][kParts], int s) {
-#pragma unroll
-  for (int i = 0; i < kTiles; i++)
-#pragma unroll
-    for (int part = 0; part < kParts; part++) {
-      const uint4 q = xv[i][part];
-      if (s == 0 && part == 0) mma_first(d[i], a, q.x, q.y);
-      else mma(d[i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
-    }
-}
 template <int kTiles, int kParts>
 __device__ __forceinline__ void read_values(uint4 xv[kTiles][kParts], uint32_t at, uint32_t tile_bytes) {
 #pragma unroll
@@ -508,35 +503,92 @@ __device__ __forceinline__ void read_values(uint4 xv[kTiles][kParts], uint32_t a
 #pragma unroll
     for (int part = 0; part < kParts; part++) xv[i][part] = shared16(at + (part * kTiles + i) * tile_bytes);
 }
+// the steps of one subtile that are not in skip (bits 0-3)
+template <int kTiles, int kParts>
+__device__ __forceinline__ void multiply_step(float d[kTiles][4], const uint32_t *a, const uint4 xv[kTiles][kParts], int s,
+                                              uint32_t skip) {
+#pragma unroll
+  for (int i = 0; i < kTiles; i++)
+#pragma unroll
+    for (int part = 0; part < kParts; part++) {
+      const uint4 q = xv[i][part];
+      mma_unless(skip & (1u << s), d[i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
+    }
+}
 
-// A warp's 16 rows of both subtiles of a stage times 8 kTiles tokens, added to
-// tot[0] and tot[1].  xs, xs2: where the tokens' values of either subtile
-// start (the same place for two matrices: kShare); tile_bytes: from 8 tokens
-// to the next 8 (then the next plane: a value is held as the sum of kParts
-// bf16 numbers).  The four products of a subtile are added up in the tensor
-// cores, subtiles in fp32 registers: the tensor cores cut off what their
-// accumulator cannot hold, so that long sums there drift toward zero.
-// Columns without a token hold sums that the caller drops.
+// What a warp needs to know of a stage.
+struct StageAt {
+  uint32_t slot, group;  // the stage's start; which 16 rows of the subtiles
+  uint32_t xs, xs2;      // the tokens' values for either subtile
+  uint32_t tile_bytes;   // from 8 tokens to the next 8, then to the next part
+  uint32_t key;          // the first subtile's
+};
+
+// A warp's 16 rows of both subtiles of a stage (or the first: only) times 8
+// kTiles tokens, added to tot0 and tot1; kShare: both take the values at xs.
+// A token's value is held as the sum of kParts bf16 numbers.  The four
+// products of a subtile are added up in the tensor cores, subtiles in fp32
+// registers: the tensor cores cut off what their accumulator cannot hold, so
+// that long sums there drift toward zero.  Columns without a token hold sums
+// that the caller drops.  unit0, unit1, row0, row1: the subtiles' units of
+// their rows, and the group's first row (for the container's lists).
 template <int kTiles, int kParts, bool kShare>
-__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], uint32_t slot, uint32_t group,
-                                              uint32_t xs, uint32_t xs2, XAt xat, uint32_t tile_bytes, uint4 book,
-                                              uint32_t lane) {
+__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, bool only,
+                                              const View &v, const Exceptions &x, uint32_t unit0, uint32_t unit1,
+                                              uint64_t row0, uint64_t row1, uint32_t K, uint32_t lane) {
+  const uint32_t steps = exceptions_steps(x, at.key, lane) & (only ? 0xFu : 0xFFu), skip = only ? steps | 0xF0u : steps;
   Piece f0, f1;
-  read_piece(f0, slot, group, lane);
-  read_piece(f1, slot + kSubBytes, group, lane);
-  float d0[kTiles][4], d1[kTiles][4];
+  read_piece(f0, at.slot, at.group, lane);
+  read_piece(f1, at.slot + kSubBytes, at.group, lane);
+  float d0[kTiles][4] = {}, d1[kTiles][4] = {};
   uint4 xv[kTiles][kParts], xw[kTiles][kParts];
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     if ((s & 1) == 0) {  // 8 values of each token, for two steps
-      read_values<kTiles, kParts>(xv, xs + (s ? xat.second : xat.first), tile_bytes);
-      if (!kShare) read_values<kTiles, kParts>(xw, xs2 + (s ? xat.second : xat.first), tile_bytes);
+      read_values<kTiles, kParts>(xv, at.xs + (s ? xat.second : xat.first), at.tile_bytes);
+      if (!kShare) read_values<kTiles, kParts>(xw, at.xs2 + (s ? xat.second : xat.first), at.tile_bytes);
     }
     uint32_t a[4], b[4];
-    expand_step(a, f0, s, book);
-    multiply_step<kTiles, kParts>(d0, a, xv, s);
-    expand_step(b, f1, s, book);
-    multiply_step<kTiles, kParts>(d1, b, kShare ? xv : xw, s);
+    expand_step(a, f0, s, v.book);
+    multiply_step<kTiles, kParts>(d0, a, xv, s, skip);
+    expand_step(b, f1, s, v.book);
+    multiply_step<kTiles, kParts>(d1, b, kShare ? xv : xw, s, skip >> 4);
+  }
+  // the steps with exceptions
+#pragma unroll 1
+  for (uint32_t rest = steps; rest; rest &= rest - 1) {
+    const uint32_t bit = __ffs(rest) - 1, sub = bit >> 2, s = bit & 3, g = lane >> 2, t = lane & 3;
+    const uint32_t from = at.slot + sub * kSubBytes;
+    uint32_t a[4];
+#pragma unroll
+    for (uint32_t h = 0; h < 2; h++) {
+      const uint32_t row = at.group * kRows + g + 8 * h;
+      const uint32_t q = shared2(from + row * 32 + 8 * t + 2 * s), lw = shared4(from + kIdxBytes + row * 64 + 16 * t + 4 * s);
+      const uint2 e = expand4(q & 0x7777u, (q >> 3) & 0x1111u, v.book, lw);
+      a[h] = e.x;
+      a[h + 2] = e.y;
+    }
+    if (x.walk) {
+      walk_patch(a, v, ((sub ? row1 : row0) + g) * K + kUnit * (sub ? unit1 : unit0) + 16 * t + 4 * s, K);
+    } else {
+      auto is = [&](uint32_t e) { return (e >> kExcKey) == at.key + sub && exc_step(e) == s; };
+      for (uint32_t hit = __ballot_sync(0xffffffffu, lane < x.cnt && is(x.e)); hit; hit &= hit - 1)
+        patch(a, __shfl_sync(0xffffffffu, x.e, __ffs(hit) - 1), lane);
+      for (uint32_t i = 32; i < x.cnt; i += 32) {
+        const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
+        for (uint32_t hit = __ballot_sync(0xffffffffu, i + lane < x.cnt && is(own)); hit; hit &= hit - 1)
+          patch(a, __shfl_sync(0xffffffffu, own, __ffs(hit) - 1), lane);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; i++)
+#pragma unroll
+      for (int part = 0; part < kParts; part++) {
+        const uint2 q = shared8((!kShare && sub ? at.xs2 : at.xs) + (s & 2 ? xat.second : xat.first) + 8 * (s & 1) +
+                                (part * kTiles + i) * at.tile_bytes);
+        if (sub) mma(d1[i], a, q.x, q.y);
+        else mma(d0[i], a, q.x, q.y);
+      }
   }
 #pragma unroll
   for (int i = 0; i < kTiles; i++)
@@ -545,48 +597,6 @@ __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[
       tot0[i][j] += d0[i][j];
       tot1[i][j] += d1[i][j];
     }
-}
-
-// One subtile, the one of exceptions x.next's key or any other; unit: which of
-// the row's, row_g: the lane's first row.
-template <int kTiles, int kParts>
-__device__ __forceinline__ void subtile_product(float tot[kTiles][4], uint32_t sub, uint32_t group, uint32_t xs, XAt xat,
-                                                uint32_t tile_bytes, const View &v, Exceptions &x, uint32_t key,
-                                                uint32_t unit, uint64_t row_g, uint32_t K, uint32_t lane) {
-  Piece f;
-  read_piece(f, sub, group, lane);
-  const bool any = key == x.next;
-  uint32_t hit = 0;  // lanes whose one is of this subtile
-  if (any && !x.walk) hit = __ballot_sync(0xffffffffu, lane < x.cnt && (x.e >> kExcKey) == key);
-  float d[kTiles][4];
-  uint4 xv[kTiles][kParts];
-#pragma unroll
-  for (int s = 0; s < 4; s++) {
-    if ((s & 1) == 0) read_values<kTiles, kParts>(xv, xs + (s ? xat.second : xat.first), tile_bytes);
-    uint32_t a[4];
-    expand_step(a, f, s, v.book);
-    if (any) {
-      if (x.walk) {
-        walk_patch(a, v, row_g * K + kUnit * unit + 16 * (lane & 3u) + 4 * s, K);
-      } else {
-        for (uint32_t rest = hit; rest; rest &= rest - 1) {
-          const uint32_t e = __shfl_sync(0xffffffffu, x.e, __ffs(rest) - 1);
-          if (exc_step(e) == uint32_t(s)) patch(a, e, lane);
-        }
-        for (uint32_t i = 32; i < x.cnt; i += 32) {
-          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
-          uint32_t rest = __ballot_sync(0xffffffffu, i + lane < x.cnt && (own >> kExcKey) == key && exc_step(own) == uint32_t(s));
-          for (; rest; rest &= rest - 1) patch(a, __shfl_sync(0xffffffffu, own, __ffs(rest) - 1), lane);
-        }
-      }
-    }
-    multiply_step<kTiles, kParts>(d, a, xv, s);
-  }
-#pragma unroll
-  for (int i = 0; i < kTiles; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) tot[i][j] += d[i][j];
-  if (any) exceptions_seek(x, key + 1, lane);
 }
 
 // A warp's sums of a group, [token][row] with kRedTok floats a token.
