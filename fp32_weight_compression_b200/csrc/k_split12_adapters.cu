@@ -177,6 +177,11 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
     uint32_t u = u0;
     for (uint32_t i = 0; i < kDepth && u < u1; i++, u += 2, turn.next()) load(u);
     ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
+    // B's rows for the tokens' adapters, on their way to L2 for the end
+    if (lane < p.M) {
+      const int32_t ad = p.adapter[lane];
+      if (ad >= 0 && ad < int32_t(p.L)) prefetch_l2(p.b + (uint64_t(ad) * p.N + n0) * p.r, kSubRows * p.r * 2);
+    }
     for (; ok && u < u1; u += 2, turn.next()) {
       if (!bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) break;
       load(u);
@@ -201,10 +206,14 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
       const XAt xat = x_boxes(lane);
       Turn turn;
       for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
+        Handed h;
+        const uint32_t most = exceptions_hand(x, h, u, lane);
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
         const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
-        stage_product<NT, 1, false>(tot0, tot1, {slot, warp, xs, xs + F::kXBox, 1024, u}, xat, u + 1 == u1, v, x, u, u + 1, row0,
-                                    row0, K, lane);
+        const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == u1, u, u, u + 1, row0, row0};
+        if (most == 1) stage_product<NT, 1, false, false>(tot0, tot1, at, xat, v.book, h, lane);
+        else if (most == 2) stage_product<NT, 1, false, true>(tot0, tot1, at, xat, v.book, h, lane);
+        else stage_product_slow<NT, 1, false>(tot0, tot1, at, xat, v, x, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
@@ -218,26 +227,49 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
     __syncwarp();
     put_sums<NT>(red + warp * F::kOwn, tot0, lane);
   }
+  // a thread has one row of every so many tokens; their adapters, and the
+  // first 16 ranks' values of B, are read before the others are waited for
+  constexpr uint32_t kOut = 8 * NT * kSubRows / kConsumers;
+  const uint32_t row = tid % kSubRows, m0 = tid / kSubRows + kConsumers / kSubRows * rank, per = kConsumers / kSubRows * csize;
+  int32_t ad[kOut];
+  uint4 b0[kOut], b1[kOut];
+  const bool puts = ok && warp < kWarps;
+#pragma unroll
+  for (uint32_t i = 0; i < kOut; i++) {
+    const uint32_t m = m0 + i * per;
+    ad[i] = puts && m < p.M ? p.adapter[m] : -1;
+    if (ad[i] >= int32_t(p.L)) ad[i] = -1;
+  }
+  auto b_of = [&](uint32_t i) { return reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad[i]) * p.N + n0 + row) * p.r); };
+#pragma unroll
+  for (uint32_t i = 0; i < kOut; i++) {
+    b0[i] = b1[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (ad[i] >= 0) {
+      b0[i] = b_of(i)[0];
+      if (p.r > 8) b1[i] = b_of(i)[1];
+    }
+  }
   if (csize > 1) cluster_sync(); else __syncthreads();
   wait_prerequisites();  // t
-  if (ok) {
-    for (uint32_t o = tid + rank * kThreads; o < 8 * NT * kSubRows; o += kThreads * csize) {
-      const uint32_t row = o % kSubRows, m = o / kSubRows;
+  if (puts) {
+#pragma unroll
+    for (uint32_t i = 0; i < kOut; i++) {
+      const uint32_t m = m0 + i * per;
       if (m >= p.M) break;
       const float *from = red + row / kRows * F::kOwn + m * kRedTok + row % kRows;
       float sum = 0.0f;
       for (uint32_t c = 0; c < csize; c++) sum += csize > 1 ? cluster_load(from, c) : *from;
-      const int32_t ad = p.adapter[m];
-      if (ad >= 0 && ad < int32_t(p.L)) {
-        const uint4 *pb = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad) * p.N + n0 + row) * p.r);
+      if (ad[i] >= 0) {
         const float4 *pt = reinterpret_cast<const float4 *>(p.t + uint64_t(m) * p.r);
         float add = 0.0f;
-        for (uint32_t j = 0; j < p.r / 8; j++) {
-          const uint4 b = pb[j];
+        auto take = [&](uint4 b, uint32_t j) {
           const float4 t0 = pt[2 * j], t1 = pt[2 * j + 1];
           add += t0.x * bf16_lo(b.x) + t0.y * bf16_hi(b.x) + t0.z * bf16_lo(b.y) + t0.w * bf16_hi(b.y);
           add += t1.x * bf16_lo(b.z) + t1.y * bf16_hi(b.z) + t1.z * bf16_lo(b.w) + t1.w * bf16_hi(b.w);
-        }
+        };
+        take(b0[i], 0);
+        if (p.r > 8) take(b1[i], 1);
+        for (uint32_t j = 2; j < p.r / 8; j++) take(b_of(i)[j], j);
         sum += add;
       }
       p.y[uint64_t(m) * p.N + n0 + row] = sum;

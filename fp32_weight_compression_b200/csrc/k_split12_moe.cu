@@ -19,10 +19,10 @@
 //     D_e of every item as through one long row, whose parts its CTAs take.
 //     The weighted sum over experts is part of the product's sum: no atomics,
 //     one rounding, one write.
-// Both find the experts from the logits themselves, a warp a token (a few
-// hundred logits), instead of waiting for a third kernel; the second starts
-// while the first one ends (programmatic dependent launch) and by then has
-// its routing, exceptions and first weights.
+// k12_moe_route finds the experts first, a warp a token.  Each kernel starts
+// while the one before it ends (programmatic dependent launch); the down
+// product's has its route, exceptions and first weights by the time that the
+// up product is done.
 #include <cstdint>
 
 #include "wc12_few.cuh"
@@ -35,35 +35,28 @@ constexpr uint32_t kMaxTokens = 32;  // of a launch
 constexpr uint32_t kMaxTop = 16;
 constexpr uint32_t kMaxExperts = 512;
 
+constexpr uint32_t kMaxPairs = kMaxTokens * kMaxTop;
+
+// The (token, expert) pairs by expert, and the items: an expert and up to 8 of
+// its pairs; experts ascending.
+struct Route {
+  float weight[kMaxPairs];   // of each pair
+  uint16_t pair[kMaxPairs];  // token * k + j, by expert
+  uint16_t item_e[kMaxPairs], item_first[kMaxPairs];
+  uint8_t item_n[kMaxPairs];
+  uint32_t items, pairs;
+};
 struct Params {
   const uint8_t *gate_up, *down;
   uint64_t gate_up_bytes, down_bytes;
   const uint16_t *x;    // [T, H]
   const float *logits;  // [T, E]
+  Route *route;
   uint16_t *hs;         // two planes of [T k, F]
   void *out;            // [T, H]
   uint32_t T, E, H, F, k;
   uint32_t renormalize, wide;
   int32_t *status;
-};
-
-constexpr uint32_t kMaxPairs = kMaxTokens * kMaxTop;
-
-// The tokens' experts, and the items: an expert and up to 8 (token, expert)
-// pairs that chose it, experts ascending.
-struct Route {
-  int16_t id[kMaxTokens][kMaxTop];  // expert, -1: none
-  float p[kMaxTokens][kMaxTop];
-  uint16_t pair[kMaxPairs];         // token * k + j, by expert
-  uint16_t item_e[kMaxPairs], item_first[kMaxPairs];
-  uint8_t item_n[kMaxPairs];
-  uint32_t items;
-};
-// while it is found (in shared memory that the ring takes later)
-struct RouteScratch {
-  uint32_t key[8192];           // of as many tokens as fit
-  uint32_t who[kMaxExperts];    // the tokens that chose each expert, a bit each
-  uint16_t first[kMaxExperts];  // their first place in pair[]
 };
 
 // ascending in the logits' order; -0 like +0, NaN above all
@@ -75,90 +68,116 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_key(-inf)
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
-__device__ void route(Route &r, RouteScratch &w, const Params &p) {
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (uint32_t e = tid; e < p.E; e += kThreads) w.who[e] = 0;
-  const uint32_t batch = 8192 / p.E;
-  for (uint32_t m0 = 0; m0 < p.T; m0 += batch) {
-    const uint32_t some = p.T - m0 < batch ? p.T - m0 : batch;
-#pragma unroll 4
-    for (uint32_t i = tid; i < some * p.E; i += kThreads) w.key[i] = order_key(p.logits[uint64_t(m0) * p.E + i]);
-    __syncthreads();
-    for (uint32_t m = m0 + warp; m < m0 + some; m += kThreads / 32) {
-      const uint32_t *key = w.key + (m - m0) * p.E;
-      uint32_t taken = 0;               // of the lane's experts
-      uint32_t mine = 0, mine_e = 0;    // lane j: the j-th largest key and its expert
-      uint32_t top = 0;
-      for (uint32_t j = 0; j < p.k; j++) {
-        uint32_t best = 0, at = 0xFFFFFFFFu;
-        for (uint32_t i = 0, e = lane; e < p.E; i++, e += 32) {
-          const uint32_t q = key[e];
-          if (!((taken >> i) & 1u) && q > best) {
-            best = q;
-            at = e;
-          }
-        }
-        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? at : 0xFFFFFFFFu);
-        if (high <= kMinusInf) break;  // only -inf is left
-        if ((e & 31u) == lane) taken |= 1u << (e >> 5);
-        if (lane == j) {
-          mine = high;
-          mine_e = e;
-        }
-        if (j == 0) top = high;
-      }
-      const float largest = key_value(top);
-      const float ex = mine != 0 ? expf(key_value(mine) - largest) : 0.0f;
-      float sum = ex;
-      if (!p.renormalize) {
-        sum = 0.0f;
-        for (uint32_t e = lane; e < p.E; e += 32) sum += expf(key_value(key[e]) - largest);
-      }
+// Finds the experts: one CTA, a warp a token, whose lanes hold kPer logits
+// each.
+template <int kPer>
+__global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_constant__ Params p) {
+  launch_dependents();
+  __shared__ uint32_t who[kMaxExperts];    // the tokens that chose each expert, a bit each
+  __shared__ uint16_t place[kMaxExperts];  // their first place in pair[]
+  Route &r = *p.route;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, m = tid >> 5;
+  uint32_t key[kPer];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane < p.k) {
-        r.id[m][lane] = mine != 0 ? int16_t(mine_e) : int16_t(-1);
-        r.p[m][lane] = ex / sum;
-        if (mine != 0) atomicOr(&w.who[mine_e], 1u << m);
-      }
-    }
-    __syncthreads();
+  for (int i = 0; i < kPer; i++) {
+    const uint32_t e = lane + 32 * i;
+    key[i] = e < p.E ? order_key(p.logits[uint64_t(m) * p.E + e]) : 0u;
   }
+  for (uint32_t e = tid; e < p.E; e += blockDim.x) who[e] = 0;
+  __syncthreads();
+  uint32_t mine = 0, mine_e = 0, top = 0;  // lane j: the j-th largest key and its expert
+  {
+    uint32_t left[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i++) left[i] = key[i];
+    for (uint32_t j = 0; j < p.k; j++) {
+      uint32_t best = 0, at = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kPer; i++)
+        if (left[i] > best) {
+          best = left[i];
+          at = lane + 32 * i;
+        }
+      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+      const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? at : 0xFFFFFFFFu);
+      if (high <= kMinusInf) break;  // only -inf is left
+#pragma unroll
+      for (int i = 0; i < kPer; i++)
+        if (e == lane + 32 * i) left[i] = 0;
+      if (lane == j) {
+        mine = high;
+        mine_e = e;
+      }
+      if (j == 0) top = high;
+    }
+  }
+  const float largest = key_value(top);
+  const float ex = mine != 0 ? expf(key_value(mine) - largest) : 0.0f;
+  float sum = ex;
+  if (!p.renormalize) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; i++)
+      if (lane + 32 * i < p.E) sum += expf(key_value(key[i]) - largest);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < p.k && mine != 0) atomicOr(&who[mine_e], 1u << m);
+  __syncthreads();
   // the experts' places in pair[], and their items
-  if (warp == 0) {
+  if (m == 0) {
     uint32_t pairs = 0, items = 0;
     for (uint32_t e0 = 0; e0 < p.E; e0 += 32) {
-      const uint32_t e = e0 + lane, n = e < p.E ? __popc(w.who[e]) : 0u, blocks = (n + 7) / 8;
-      uint32_t a = n, b = blocks;
+      const uint32_t e = e0 + lane, n = e < p.E ? __popc(who[e]) : 0u, blocks = (n + 7) / 8;
+      if (__all_sync(0xffffffffu, n == 0)) continue;
+      uint32_t both = n | (blocks << 16);  // both at most 512
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= uint32_t(o)) {
-          a += x;
-          b += y;
-        }
+        const uint32_t u = __shfl_up_sync(0xffffffffu, both, o);
+        if (lane >= uint32_t(o)) both += u;
       }
-      const uint32_t first = pairs + a - n;
-      if (e < p.E) w.first[e] = uint16_t(first);
+      const uint32_t first = pairs + (both & 0xFFFFu) - n, at = items + (both >> 16) - blocks;
+      if (n > 0) place[e] = uint16_t(first);
       for (uint32_t i = 0; i < blocks; i++) {
-        const uint32_t at = items + b - blocks + i;
-        r.item_e[at] = uint16_t(e);
-        r.item_first[at] = uint16_t(first + 8 * i);
-        r.item_n[at] = uint8_t(n - 8 * i < 8 ? n - 8 * i : 8);
+        r.item_e[at + i] = uint16_t(e);
+        r.item_first[at + i] = uint16_t(first + 8 * i);
+        r.item_n[at + i] = uint8_t(n - 8 * i < 8 ? n - 8 * i : 8);
       }
-      pairs += __shfl_sync(0xffffffffu, a, 31);
-      items += __shfl_sync(0xffffffffu, b, 31);
+      both = __shfl_sync(0xffffffffu, both, 31);
+      pairs += both & 0xFFFFu;
+      items += both >> 16;
     }
-    if (lane == 0) r.items = items;
+    if (lane == 0) {
+      r.items = items;
+      r.pairs = pairs;
+    }
   }
   __syncthreads();
-  // by token within an expert, so that every CTA has the same items
-  for (uint32_t i = tid; i < p.T * p.k; i += kThreads) {
-    const int32_t e = r.id[i / p.k][i % p.k];
-    if (e >= 0) r.pair[w.first[e] + __popc(w.who[e] & ((1u << i / p.k) - 1u))] = uint16_t(i);
+  // by token within an expert
+  if (lane < p.k && mine != 0) {
+    const uint32_t at = place[mine_e] + __popc(who[mine_e] & ((1u << m) - 1u));
+    r.pair[at] = uint16_t(m * p.k + lane);
+    r.weight[at] = ex / sum;
   }
-  __syncthreads();
+}
+
+// The route, as the two products have it: from the workspace into shared
+// memory, what there is of it (every thread; a barrier has to follow).
+__device__ __forceinline__ void take_route(Route &r, const Route *from) {
+  const uint32_t tid = threadIdx.x, items = from->items, pairs = from->pairs;
+  for (uint32_t i = tid; i < items; i += kThreads) {
+    r.item_e[i] = from->item_e[i];
+    r.item_first[i] = from->item_first[i];
+    r.item_n[i] = from->item_n[i];
+  }
+  for (uint32_t i = tid; i < pairs; i += kThreads) {
+    r.pair[i] = from->pair[i];
+    r.weight[i] = from->weight[i];
+  }
+  if (tid == 0) {
+    r.items = items;
+    r.pairs = pairs;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -172,7 +191,6 @@ struct Up {
   static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = kBars + sizeof(Bars);
 };
-static_assert(sizeof(RouteScratch) <= Up::kRoute, "scratch");
 
 // p_e silu(gate) up as two bf16 numbers, each rounded to nearest: off by at
 // most 2^-18 of it
@@ -186,7 +204,6 @@ __device__ __forceinline__ void put_gated(uint16_t *dst, uint64_t plane, float g
 // A stage's two subtiles: 64 rows of G_e and of U_e, the same values of H.
 __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant__ Params p,
                                                           const __grid_constant__ Planes planes, uint32_t csize) {
-  launch_dependents();
   extern __shared__ __align__(128) uint8_t dyn[];
   Route &r = *reinterpret_cast<Route *>(dyn + Up::kRoute);
   Bars &bars = *reinterpret_cast<Bars *>(dyn + Up::kBars);
@@ -196,7 +213,10 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   open_planes(v, p.gate_up, uint64_t(p.E) * 2 * p.F * p.H);
   const bool ok = open_header(v, p.gate_up, p.gate_up_bytes);  // the same for every thread
   if (tid == 0) bars_init(bars);
-  route(r, *reinterpret_cast<RouteScratch *>(dyn), p);
+  wait_prerequisites();  // the route
+  launch_dependents();   // the down product's CTAs, which read the route too
+  take_route(r, p.route);
+  __syncthreads();
   if (!ok) {
     if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
     return;
@@ -205,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   const uint32_t tiles = p.F / kSubRows, jobs = r.items * tiles, ring = smem_u32(dyn);
   Turn turn;
   if (warp == kWarps) {
-    fence_async();  // the routing's scratch was in the ring
     uint32_t s = 0;
     bool alive = true;
     for (uint32_t job = first; alive && job < jobs; job += clusters) {
@@ -274,11 +293,15 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
     offsets(next, job + 2 * clusters);
     float gate[1][4] = {}, up[1][4] = {};
     for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
+      Handed h;
+      const uint32_t most = exceptions_hand(x, h, 2 * u, lane);
       alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
-      stage_product<1, 1, true>(gate, up, {slot, warp, xs, xs, 0, 2 * u}, xat, false, v, x, u, u, row_of(job, 0), row_of(job, 1), K,
-                                lane);
+      const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
+      if (most == 1) stage_product<1, 1, true, false>(gate, up, at, xat, v.book, h, lane);
+      else if (most == 2) stage_product<1, 1, true, true>(gate, up, at, xat, v.book, h, lane);
+      else stage_product_slow<1, 1, true>(gate, up, at, xat, v, x, K, lane);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
         const uint32_t c = 2 * t + (i & 1), row = f0 + kRows * warp + g + 8 * (i >> 1);
         if (c < n) {
           const uint32_t pair = r.pair[from + c];
-          put_gated(p.hs + uint64_t(pair) * p.F + row, plane, gate[0][i], up[0][i], r.p[pair / p.k][pair % p.k]);
+          put_gated(p.hs + uint64_t(pair) * p.F + row, plane, gate[0][i], up[0][i], r.weight[from + c]);
         }
       }
       continue;
@@ -307,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
         b += cluster_load(at + 8 * kRedTok, i);
       }
       const uint32_t pair = r.pair[from + c];
-      put_gated(p.hs + uint64_t(pair) * p.F + f0 + row, plane, a, b, r.p[pair / p.k][pair % p.k]);
+      put_gated(p.hs + uint64_t(pair) * p.F + f0 + row, plane, a, b, r.weight[from + c]);
     }
     cluster_sync();  // the others' sums are read until here
   }
@@ -323,7 +346,6 @@ struct Down {
   static constexpr uint32_t kAcc = align128(kBars + uint32_t(sizeof(Bars)));
   static __host__ __device__ uint32_t smem(uint32_t T) { return kAcc + kWarps * T * kRedTok * 4; }
 };
-static_assert(sizeof(RouteScratch) <= Down::kRoute, "scratch");
 
 __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constant__ Params p,
                                                             const __grid_constant__ Planes planes, uint32_t csize) {
@@ -339,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
   if (warp < kWarps)
     for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
-  route(r, *reinterpret_cast<RouteScratch *>(dyn), p);
+  take_route(r, p.route);  // the up product's CTAs had it before this one could start
+  __syncthreads();
   // the items' stages one after another; this CTA's: [q0, q1)
   const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2, all = r.items * per, ring = smem_u32(dyn);
   const uint32_t q0 = ok ? uint32_t(uint64_t(all) * rank / csize) : 0u, q1 = ok ? uint32_t(uint64_t(all) * (rank + 1) / csize) : 0u;
@@ -347,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
   Turn turn;
   if (warp == kWarps) {
-    fence_async();  // the routing's scratch was in the ring
     const uint64_t plane = uint64_t(p.T) * p.k * p.F;
     struct At {
       uint32_t item, st;
@@ -428,11 +450,15 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       offsets(next, item + 2);
       float tot0[1][4] = {}, tot1[1][4] = {};
       for (; st < end; st++, q++, turn.next()) {
+        Handed h;
+        const uint32_t most = exceptions_hand(x, h, 2 * st, lane);
         alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
         if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
-        stage_product<1, 2, false>(tot0, tot1, {slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u}, xat, u + 1 == units, v, x, u, u + 1,
-                                   row_of(item), row_of(item), K, lane);
+        const StageAt at{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row_of(item), row_of(item)};
+        if (most == 1) stage_product<1, 2, false, false>(tot0, tot1, at, xat, v.book, h, lane);
+        else if (most == 2) stage_product<1, 2, false, true>(tot0, tot1, at, xat, v.book, h, lane);
+        else stage_product_slow<1, 2, false>(tot0, tot1, at, xat, v, x, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
@@ -469,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
 
 extern "C" uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F) {
   const uint64_t t = T < wc12m::kMaxTokens ? T : wc12m::kMaxTokens;
-  return t * k * F * 4;
+  return wc12m::align128(sizeof(wc12m::Route)) + t * k * F * 4;
 }
 
 extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const void *d_down, uint64_t down_bytes,
@@ -498,7 +524,8 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   p.gate_up_bytes = gate_up_bytes;
   p.down = static_cast<const uint8_t *>(d_down);
   p.down_bytes = down_bytes;
-  p.hs = static_cast<uint16_t *>(d_work);
+  p.route = static_cast<Route *>(d_work);
+  p.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(d_work) + align128(sizeof(Route)));
   p.E = E;
   p.H = H;
   p.F = F;
@@ -528,7 +555,10 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
     uint32_t cd = 1;
     while (cd < 8 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
-    if (launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < slots ? jobs : slots), kThreads, cu, Up::kSmem, s, false, p, up, cu) !=
+    const uint32_t per = (E + 31) / 32;  // logits of a lane
+    auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
+    if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
+        launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < slots ? jobs : slots), kThreads, cu, Up::kSmem, s, true, p, up, cu) !=
             cudaSuccess ||
         launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;

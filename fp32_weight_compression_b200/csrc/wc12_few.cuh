@@ -33,9 +33,9 @@
 // container's per-chunk lists, 64 entries a load, while its first weights are
 // in flight (or the ones of the rows before), and keeps those of its part of
 // K, one a lane.  More than its list holds: it looks each lane's values up in
-// the container's sorted lists instead (slow, and right for any container).  The
-// products are made by code without a branch, but for the steps that have an
-// exception, which are left out there and made by a loop behind it.
+// the container's sorted lists instead (slow, and right for any container).  A
+// stage's entries are handed to the lanes that hold their values before the
+// products, which then take them in passing, without a branch.
 #pragma once
 
 #include <cstdint>
@@ -179,6 +179,10 @@ __device__ __forceinline__ uint2 shared8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+
+// A warp's own part of shared memory: its list of exceptions, then its sums.
+constexpr uint32_t own_words(uint32_t tokens) { return tokens * kRedTok > kListCap ? tokens * kRedTok : kListCap; }
+
 __device__ __forceinline__ uint32_t shared4(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -189,9 +193,6 @@ __device__ __forceinline__ uint32_t shared2(uint32_t a) {
   asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a));
   return v;
 }
-
-// A warp's own part of shared memory: its list of exceptions, then its sums.
-constexpr uint32_t own_words(uint32_t tokens) { return tokens * kRedTok > kListCap ? tokens * kRedTok : kListCap; }
 
 struct Bars {
   uint64_t full[kDepth], empty[kDepth];
@@ -271,6 +272,9 @@ __device__ __forceinline__ void load_row(uint32_t dst, const void *src, uint32_t
                ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {  // a multiple of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 // what threads wrote to the ring before is done before a copy writes there
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -290,12 +294,17 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
 
 // wc12::expand4 with the selectors of 8 nibbles split beforehand: sel is the
 // entry within its half (3 bits), up 1 for entries 8..15, in the low 16 bits
-__device__ __forceinline__ uint2 expand4(uint32_t sel, uint32_t up, uint4 book, uint32_t lo4) {
+__device__ __forceinline__ uint32_t high4(uint32_t sel, uint32_t up, uint4 book) {
   const uint32_t r0 = prmt(book.x, book.y, sel);
   const uint32_t r1 = prmt(book.z, book.w, sel);
   const uint32_t m = prmt(0x0000FF00u, 0u, up);
-  const uint32_t hi4 = (r0 & ~m) | (r1 & m);
+  return (r0 & ~m) | (r1 & m);
+}
+__device__ __forceinline__ uint2 join4(uint32_t lo4, uint32_t hi4) {
   return make_uint2(prmt(lo4, hi4, 0x5140), prmt(lo4, hi4, 0x7362));
+}
+__device__ __forceinline__ uint2 expand4(uint32_t sel, uint32_t up, uint4 book, uint32_t lo4) {
+  return join4(lo4, high4(sel, up, book));
 }
 
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -304,15 +313,6 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// unless skip (the same for the whole warp)
-__device__ __forceinline__ void mma_unless(uint32_t skip, float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %10, 0;\n\t"
-      "@p mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};\n\t}"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(skip));
-}
-
 // ---------------------------------------------------------------------------
 // Exceptions.  An entry: high byte (bits 0-7), row of the group (8-11),
 // column of the unit (12-17), key (18-31): which subtile of the warp's rows,
@@ -321,16 +321,16 @@ constexpr uint32_t kExcKey = 18;
 __device__ __forceinline__ uint32_t pack_exc(uint32_t key, uint32_t col, uint32_t row, uint32_t high) {
   return high | (row << 8) | (col << 12) | (key << kExcKey);
 }
-__device__ __forceinline__ uint32_t exc_step(uint32_t e) { return (e >> 14) & 3u; }  // the product that uses it
-// puts the entry's high byte into the A words of its step, in its lane
-__device__ __forceinline__ void patch(uint32_t *a, uint32_t e, uint32_t lane) {
-  const uint32_t owner = ((e >> 8) & 7u) * 4 + ((e >> 16) & 3u);
-  if (lane != owner) return;
-  const uint32_t word = ((e >> 11) & 1u) | ((e >> 12) & 2u);  // row half, then the pair of the step
-  const uint32_t sel = (e >> 12) & 1u ? 0x4210u : 0x3240u;     // the pair's second or first value
-#pragma unroll
-  for (uint32_t i = 0; i < 4; i++)
-    if (word == i) a[i] = prmt(a[i], e, sel);
+// An entry as its lane uses it: the place among the 16 sets of 4 values that
+// it has of a stage (8 subtile + 2 step + row half), and which of the 4.
+__device__ __forceinline__ uint32_t exc_owner(uint32_t e) { return ((e >> 8) & 7u) * 4 + ((e >> 16) & 3u); }
+__device__ __forceinline__ uint32_t exc_place(uint32_t e, uint32_t key) {
+  return (((e >> kExcKey) - key) << 3) | ((e >> 13) & 6u) | ((e >> 11) & 1u);
+}
+// selects the entry's byte in the place of value i of 4: prmt(hi4, e, ..)
+__device__ __forceinline__ uint32_t exc_select(uint32_t e) {
+  const uint32_t i = 4 * ((e >> 12) & 3u);
+  return (0x3210u & ~(0xFu << i)) | (4u << i);
 }
 
 // The container's exceptions around a group of 16 rows, in flight: lane j
@@ -414,17 +414,54 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
     }
   }
 }
-// the steps of subtiles key (bits 0-3) and key + 1 (4-7) that have one
-__device__ __forceinline__ uint32_t exceptions_steps(const Exceptions &x, uint32_t key, uint32_t lane) {
-  if (x.walk) return 0xFFu;
-  if (x.cnt == 0) return 0;
-  auto bit = [&](uint32_t e) {
-    const uint32_t d = (e >> kExcKey) - key;
-    return d < 2 ? 1u << (4 * d + exc_step(e)) : 0u;
+// A stage's exceptions (subtiles key and key + 1), handed to their lanes: the
+// first of a lane, and the second, is e and select at place (16: none).
+// Returns 1, or if a lane has two 2, or if one has more (or walk) 3.
+struct Handed {
+  uint32_t place, e, select, place2, e2;
+};
+__device__ __forceinline__ uint32_t exceptions_hand(const Exceptions &x, Handed &h, uint32_t key, uint32_t lane) {
+  h.place = h.place2 = 16;
+  h.e = h.select = h.e2 = 0;
+  uint32_t most = x.walk ? 3 : 0;
+  auto hand = [&](uint32_t own, bool in) {
+    uint32_t hit = __ballot_sync(0xffffffffu, in && (own >> kExcKey) - key < 2);
+    for (; hit; hit &= hit - 1) {
+      const uint32_t e = __shfl_sync(0xffffffffu, own, __ffs(hit) - 1);
+      if (exc_owner(e) == lane) {
+        most++;
+        h.place2 = h.place;
+        h.e2 = h.e;
+        h.place = exc_place(e, key);
+        h.e = e;
+        h.select = exc_select(e);
+      }
+    }
   };
-  uint32_t b = lane < x.cnt ? bit(x.e) : 0u;
-  for (uint32_t i = 32 + lane; i < x.cnt; i += 32) b |= bit(x.list[i]);
-  return __reduce_or_sync(0xffffffffu, b);
+  if (x.cnt > 0) hand(x.e, lane < x.cnt);
+  for (uint32_t i = 32; i < x.cnt; i += 32) hand(i + lane < x.cnt ? x.list[i + lane] : 0u, i + lane < x.cnt);
+  return __any_sync(0xffffffffu, most > 1) ? __any_sync(0xffffffffu, most > 2) ? 3 : 2 : 1;
+}
+// The container's exceptions among 4 values, the first at flat position f,
+// onto their high bytes.
+static __device__ __noinline__ uint32_t exceptions_walk(uint32_t hi4, const uint64_t *exc_off, const uint16_t *exc_pos,
+                                                        const uint8_t *exc_val, uint64_t ne, uint64_t f) {
+  const uint64_t c = f / kChunk;
+  const uint32_t pos = uint32_t(f % kChunk);
+  uint64_t lo = exc_off[c], hi = exc_off[c + 1];
+  if (lo > hi || hi > ne) hi = lo = 0;
+  const uint64_t end = hi;
+  while (lo < hi) {
+    const uint64_t mid = (lo + hi) >> 1;
+    if (exc_pos[mid] < pos) lo = mid + 1; else hi = mid;
+  }
+  for (uint64_t e = lo; e < end && e < lo + 4; e++) {
+    const uint32_t p = exc_pos[e];
+    if (p < pos || p >= pos + 4) break;
+    const uint32_t i = 4 * (p - pos);
+    hi4 = prmt(hi4, exc_val[e], (0x3210u & ~(0xFu << i)) | (4u << i));
+  }
+  return hi4;
 }
 __device__ __forceinline__ void exceptions_reset(Exceptions &x) {
   x.cnt = 0;
@@ -435,39 +472,6 @@ __device__ __forceinline__ void exceptions_reset(Exceptions &x) {
 __device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
   __syncwarp();
   x.e = lane < x.cnt ? x.list[lane] : 0u;
-}
-
-// Replaces the high bytes of a lane's words of a step by the exceptions that
-// the container lists: 4 values of rows g and g + 8, row g's first one at flat
-// position f (a multiple of 4).
-static __device__ __noinline__ uint2 walk_find(const uint64_t *exc_off, const uint16_t *exc_pos, const uint8_t *exc_val,
-                                        uint64_t ne, uint64_t f) {
-  const uint64_t c = f / kChunk;
-  const uint32_t pos = uint32_t(f % kChunk);
-  uint64_t lo = exc_off[c], hi = exc_off[c + 1];
-  if (lo > hi || hi > ne) hi = lo = 0;
-  const uint64_t end = hi;
-  while (lo < hi) {
-    const uint64_t mid = (lo + hi) >> 1;
-    if (exc_pos[mid] < pos) lo = mid + 1; else hi = mid;
-  }
-  uint2 m = make_uint2(0u, 0u);  // which of the 4, their high bytes
-  for (uint64_t e = lo; e < end && e < lo + 4; e++) {
-    const uint32_t p = exc_pos[e];
-    if (p < pos || p >= pos + 4) break;
-    m.x |= 1u << (p - pos);
-    m.y |= uint32_t(exc_val[e]) << (8 * (p - pos));
-  }
-  return m;
-}
-__device__ __forceinline__ void walk_patch(uint32_t *a, const View &v, uint64_t f, uint32_t K) {
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const uint2 m = walk_find(v.exc_off, v.exc_pos, v.exc_val, v.ne, f + h * (uint64_t(K) * 8));
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      if ((m.x >> i) & 1u) a[h + 2 * (i >> 1)] = prmt(a[h + 2 * (i >> 1)], m.y >> (8 * i), i & 1 ? 0x4210u : 0x3240u);
-  }
 }
 
 // A lane's 16 values of two rows of a subtile, as stored.
@@ -484,18 +488,6 @@ __device__ __forceinline__ void read_piece(Piece &f, uint32_t sub, uint32_t grou
     f.lo[h] = shared16(sub + kIdxBytes + (group * kRows + g + 8 * h) * 64 + 16 * t);
   }
 }
-// the A fragment of step s (a constant once unrolled)
-__device__ __forceinline__ void expand_step(uint32_t *a, const Piece &f, int s, uint4 book) {
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const uint32_t qw = s < 2 ? f.idx[h].x : f.idx[h].y;
-    const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
-    const uint32_t lw = s == 0 ? f.lo[h].x : s == 1 ? f.lo[h].y : s == 2 ? f.lo[h].z : f.lo[h].w;
-    const uint2 e = expand4(sel, up, book, lw);
-    a[h] = e.x;
-    a[h + 2] = e.y;
-  }
-}
 template <int kTiles, int kParts>
 __device__ __forceinline__ void read_values(uint4 xv[kTiles][kParts], uint32_t at, uint32_t tile_bytes) {
 #pragma unroll
@@ -503,100 +495,121 @@ __device__ __forceinline__ void read_values(uint4 xv[kTiles][kParts], uint32_t a
 #pragma unroll
     for (int part = 0; part < kParts; part++) xv[i][part] = shared16(at + (part * kTiles + i) * tile_bytes);
 }
-// the steps of one subtile that are not in skip (bits 0-3)
-template <int kTiles, int kParts>
-__device__ __forceinline__ void multiply_step(float d[kTiles][4], const uint32_t *a, const uint4 xv[kTiles][kParts], int s,
-                                              uint32_t skip) {
-#pragma unroll
-  for (int i = 0; i < kTiles; i++)
-#pragma unroll
-    for (int part = 0; part < kParts; part++) {
-      const uint4 q = xv[i][part];
-      mma_unless(skip & (1u << s), d[i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
-    }
-}
-
 // What a warp needs to know of a stage.
 struct StageAt {
-  uint32_t slot, group;  // the stage's start; which 16 rows of the subtiles
-  uint32_t xs, xs2;      // the tokens' values for either subtile
-  uint32_t tile_bytes;   // from 8 tokens to the next 8, then to the next part
-  uint32_t key;          // the first subtile's
+  uint32_t slot, group;   // the stage's start; which 16 rows of the subtiles
+  uint32_t xs, xs2;       // the tokens' values for either subtile
+  uint32_t tile_bytes;    // from 8 tokens to the next 8, then to the next part
+  bool only;              // the first subtile only
+  uint32_t key;           // the first subtile's
+  uint32_t unit0, unit1;  // which units of their rows the subtiles are,
+  uint64_t row0, row1;    // and the group's first row (for the container's lists)
 };
 
-// A warp's 16 rows of both subtiles of a stage (or the first: only) times 8
-// kTiles tokens, added to tot0 and tot1; kShare: both take the values at xs.
-// A token's value is held as the sum of kParts bf16 numbers.  The four
-// products of a subtile are added up in the tensor cores, subtiles in fp32
-// registers: the tensor cores cut off what their accumulator cannot hold, so
-// that long sums there drift toward zero.  Columns without a token hold sums
-// that the caller drops.  unit0, unit1, row0, row1: the subtiles' units of
-// their rows, and the group's first row (for the container's lists).
-template <int kTiles, int kParts, bool kShare>
-__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, bool only,
-                                              const View &v, const Exceptions &x, uint32_t unit0, uint32_t unit1,
-                                              uint64_t row0, uint64_t row1, uint32_t K, uint32_t lane) {
-  const uint32_t steps = exceptions_steps(x, at.key, lane) & (only ? 0xFu : 0xFFu), skip = only ? steps | 0xF0u : steps;
-  Piece f0, f1;
-  read_piece(f0, at.slot, at.group, lane);
-  read_piece(f1, at.slot + kSubBytes, at.group, lane);
-  float d0[kTiles][4] = {}, d1[kTiles][4] = {};
-  uint4 xv[kTiles][kParts], xw[kTiles][kParts];
+// A warp's 16 rows of both subtiles of a stage times 8 kTiles tokens, added to
+// tot0 and tot1; kShare: both take the values at xs.  A token's value is held
+// as the sum of kParts bf16 numbers.  The four products of a subtile are
+// added up in the tensor cores, subtiles in fp32 registers: the tensor cores
+// cut off what their accumulator cannot hold, so that long sums there drift
+// toward zero.  Columns without a token hold sums that the caller drops.
+// kTwo: a lane may have two exceptions (one stage in a hundred, where the
+// containers have one in 2,500 values; four warps share a stage, so that code
+// which is slow one time in a hundred is felt).
+template <int kTiles, int kParts, bool kShare, bool kTwo>
+__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, uint4 book,
+                                              const Handed &h, uint32_t lane) {
+  Piece f[2];
+  read_piece(f[0], at.slot, at.group, lane);
+  read_piece(f[1], at.slot + kSubBytes, at.group, lane);
+  float d[2][kTiles][4] = {};
+  uint4 xv[2][kTiles][kParts];
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     if ((s & 1) == 0) {  // 8 values of each token, for two steps
-      read_values<kTiles, kParts>(xv, at.xs + (s ? xat.second : xat.first), at.tile_bytes);
-      if (!kShare) read_values<kTiles, kParts>(xw, at.xs2 + (s ? xat.second : xat.first), at.tile_bytes);
+      read_values<kTiles, kParts>(xv[0], at.xs + (s ? xat.second : xat.first), at.tile_bytes);
+      if (!kShare) read_values<kTiles, kParts>(xv[1], at.xs2 + (s ? xat.second : xat.first), at.tile_bytes);
     }
-    uint32_t a[4], b[4];
-    expand_step(a, f0, s, v.book);
-    multiply_step<kTiles, kParts>(d0, a, xv, s, skip);
-    expand_step(b, f1, s, v.book);
-    multiply_step<kTiles, kParts>(d1, b, kShare ? xv : xw, s, skip >> 4);
-  }
-  // the steps with exceptions
-#pragma unroll 1
-  for (uint32_t rest = steps; rest; rest &= rest - 1) {
-    const uint32_t bit = __ffs(rest) - 1, sub = bit >> 2, s = bit & 3, g = lane >> 2, t = lane & 3;
-    const uint32_t from = at.slot + sub * kSubBytes;
-    uint32_t a[4];
 #pragma unroll
-    for (uint32_t h = 0; h < 2; h++) {
-      const uint32_t row = at.group * kRows + g + 8 * h;
-      const uint32_t q = shared2(from + row * 32 + 8 * t + 2 * s), lw = shared4(from + kIdxBytes + row * 64 + 16 * t + 4 * s);
-      const uint2 e = expand4(q & 0x7777u, (q >> 3) & 0x1111u, v.book, lw);
-      a[h] = e.x;
-      a[h + 2] = e.y;
-    }
-    if (x.walk) {
-      walk_patch(a, v, ((sub ? row1 : row0) + g) * K + kUnit * (sub ? unit1 : unit0) + 16 * t + 4 * s, K);
-    } else {
-      auto is = [&](uint32_t e) { return (e >> kExcKey) == at.key + sub && exc_step(e) == s; };
-      for (uint32_t hit = __ballot_sync(0xffffffffu, lane < x.cnt && is(x.e)); hit; hit &= hit - 1)
-        patch(a, __shfl_sync(0xffffffffu, x.e, __ffs(hit) - 1), lane);
-      for (uint32_t i = 32; i < x.cnt; i += 32) {
-        const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
-        for (uint32_t hit = __ballot_sync(0xffffffffu, i + lane < x.cnt && is(own)); hit; hit &= hit - 1)
-          patch(a, __shfl_sync(0xffffffffu, own, __ffs(hit) - 1), lane);
+    for (int sub = 0; sub < 2; sub++) {
+      uint32_t a[4];
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        const uint32_t qw = s < 2 ? f[sub].idx[r].x : f[sub].idx[r].y;
+        const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
+        const uint32_t lw = s == 0 ? f[sub].lo[r].x : s == 1 ? f[sub].lo[r].y : s == 2 ? f[sub].lo[r].z : f[sub].lo[r].w;
+        uint32_t hi4 = high4(sel, up, book);
+        hi4 = h.place == uint32_t(8 * sub + 2 * s + r) ? prmt(hi4, h.e, h.select) : hi4;
+        if (kTwo) hi4 = h.place2 == uint32_t(8 * sub + 2 * s + r) ? prmt(hi4, h.e2, exc_select(h.e2)) : hi4;
+        const uint2 e = join4(lw, hi4);
+        a[r] = e.x;
+        a[r + 2] = e.y;
       }
+#pragma unroll
+      for (int i = 0; i < kTiles; i++)
+#pragma unroll
+        for (int part = 0; part < kParts; part++) {
+          const uint4 q = xv[kShare ? 0 : sub][i][part];
+          mma(d[sub][i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kTiles; i++)
-#pragma unroll
-      for (int part = 0; part < kParts; part++) {
-        const uint2 q = shared8((!kShare && sub ? at.xs2 : at.xs) + (s & 2 ? xat.second : xat.first) + 8 * (s & 1) +
-                                (part * kTiles + i) * at.tile_bytes);
-        if (sub) mma(d1[i], a, q.x, q.y);
-        else mma(d0[i], a, q.x, q.y);
-      }
   }
 #pragma unroll
   for (int i = 0; i < kTiles; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      tot0[i][j] += d0[i][j];
-      tot1[i][j] += d1[i][j];
+      tot0[i][j] += d[0][i][j];
+      if (!at.only) tot1[i][j] += d[1][i][j];
     }
+}
+
+// The same for a stage with more exceptions than two a lane, a step at a time.
+template <int kTiles, int kParts, bool kShare>
+__device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat,
+                                                   const View &v, const Exceptions &x, uint32_t K, uint32_t lane) {
+  const uint32_t g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (uint32_t step = 0; step < (at.only ? 4 : 8); step++) {
+    const uint32_t sub = step >> 2, s = step & 3, from = at.slot + sub * kSubBytes;
+    uint32_t a[4];
+#pragma unroll
+    for (uint32_t r = 0; r < 2; r++) {
+      const uint32_t row = at.group * kRows + g + 8 * r;
+      const uint32_t q = shared2(from + row * 32 + 8 * t + 2 * s), lw = shared4(from + kIdxBytes + row * 64 + 16 * t + 4 * s);
+      uint32_t hi4 = high4(q & 0x7777u, (q >> 3) & 0x1111u, v.book);
+      if (x.walk) {
+        const uint64_t at_row = (sub ? at.row1 : at.row0) + g + 8 * r;
+        hi4 = exceptions_walk(hi4, v.exc_off, v.exc_pos, v.exc_val, v.ne,
+                              at_row * K + kUnit * (sub ? at.unit1 : at.unit0) + 16 * t + 4 * s);
+      } else {
+        for (uint32_t i = 0; i < x.cnt; i += 32) {
+          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
+          uint32_t hit = __ballot_sync(0xffffffffu, i + lane < x.cnt && (exc_place(own, at.key) == 8 * sub + 2 * s + r));
+          for (; hit; hit &= hit - 1) {
+            const uint32_t e = __shfl_sync(0xffffffffu, own, __ffs(hit) - 1);
+            if (exc_owner(e) == lane) hi4 = prmt(hi4, e, exc_select(e));
+          }
+        }
+      }
+      const uint2 e = join4(lw, hi4);
+      a[r] = e.x;
+      a[r + 2] = e.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; i++) {
+      float d[4] = {};
+#pragma unroll
+      for (int part = 0; part < kParts; part++) {
+        const uint2 q = shared8((!kShare && sub ? at.xs2 : at.xs) + (s & 2 ? xat.second : xat.first) + 8 * (s & 1) +
+                                (part * kTiles + i) * at.tile_bytes);
+        mma(d, a, q.x, q.y);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        tot0[i][j] += sub ? 0.0f : d[j];
+        tot1[i][j] += sub ? d[j] : 0.0f;
+      }
+    }
+  }
 }
 
 // A warp's sums of a group, [token][row] with kRedTok floats a token.
