@@ -278,6 +278,17 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
   if (csize > 1) cluster_sync();  // the others' sums are read until here
 }
 
+// the device's SMs, the kernels set up
+int device_sms() {
+  static DeviceSetup setup;
+  return setup.get([] {
+    return cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) == cudaSuccess &&
+                   cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) ==
+                       cudaSuccess
+               ? wc12l::device_sms() : 0;
+  });
+}
+
 template <int NT>
 int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   using F = Few<NT>;
@@ -286,8 +297,6 @@ int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   if (!make_planes(planes, p.w, p.N, p.K) ||
       !wc12l::make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, p.K, p.M, uint64_t(p.K) * 2, kUnit, 8 * NT,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
-    return WC_ERR_CUDA;
-  if (cudaFuncSetAttribute(k12_few_adapters<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::kSmem)) != cudaSuccess)
     return WC_ERR_CUDA;
   // CTAs that split K: as many as run at once (4 an SM), while each fills
   // its ring
@@ -378,7 +387,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > kMaxK || N / (kRows * kSideWarps) > 65535 || M > 0x7FFFFFFFu)
     return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_linear_adapters_work_bytes(M, r)) return WC_ERR_CAPACITY;
-  const int sms = wc12l::device_sms();
+  const int sms = device_sms();
   if (sms <= 0) return WC_ERR_CUDA;
   Params p;
   p.w = static_cast<const uint8_t *>(d_w);

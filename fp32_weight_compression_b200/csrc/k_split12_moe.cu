@@ -491,6 +491,20 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   if (csize > 1) cluster_sync();  // the others' sums are read until here
 }
 
+// the CTAs of the up product that run at once on the device, the kernels set
+// up
+int up_slots() {
+  static DeviceSetup setup;
+  return setup.get([] {
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess)
+      return 0;
+    return per_sm * wc12l::device_sms();
+  });
+}
+
 }  // namespace wc12m
 
 extern "C" uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F) {
@@ -517,7 +531,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   if (d_x == nullptr || d_logits == nullptr || d_out == nullptr || d_work == nullptr) return WC_ERR_INVALID_ARG;
   if (!aligned(d_x, 16) || !aligned(d_logits, 4) || !aligned(d_out, 4) || !aligned(d_work, 16)) return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_moe_work_bytes(T, k, F)) return WC_ERR_CAPACITY;
-  const int sms = wc12l::device_sms();
+  const int slots = up_slots(), sms = slots > 0 ? wc12l::device_sms() : 0;
   if (sms <= 0) return WC_ERR_CUDA;
   Params p;
   p.gate_up = static_cast<const uint8_t *>(d_gate_up);
@@ -534,11 +548,6 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   p.wide = out_dtype == WC_FP32;
   p.status = d_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int up_per_sm = 0;
-  if (cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) != cudaSuccess ||
-      cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&up_per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess || up_per_sm < 1)
-    return WC_ERR_CUDA;
   Planes up, down;
   if (!make_planes(up, d_gate_up, uint64_t(E) * 2 * F, H) || !make_planes(down, d_down, uint64_t(E) * H, F)) return WC_ERR_CUDA;
   for (uint32_t m = 0; m < T; m += kMaxTokens) {
@@ -548,7 +557,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     p.out = static_cast<uint8_t *>(d_out) + uint64_t(m) * H * (p.wide ? 4 : 2);
     // up: clusters that split H until about 4 CTAs an SM have work; with
     // more jobs than that, as many CTAs as run at once
-    const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows), slots = uint32_t(sms * up_per_sm);
+    const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows);
     uint32_t cu = 1;
     while (cu < 8 && jobs * cu * 2 <= 4u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
     // down: CTAs that split the items, the same
@@ -558,7 +567,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
-        launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < slots ? jobs : slots), kThreads, cu, Up::kSmem, s, true, p, up, cu) !=
+        launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, Up::kSmem, s, true, p, up, cu) !=
             cudaSuccess ||
         launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;

@@ -39,11 +39,18 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 
 #include <cuda.h>
 
 #include "wc.h"
 #include "wc_split12.cuh"
+
+namespace wc {
+// Identity of the CUDA context current on this thread, 0 if none
+// (csrc/wc_noalloc.cu).
+unsigned long long current_context_id();
+}  // namespace wc
 
 namespace wc12l {
 // k_split12_linear.cu: a 2-D tensor map; the device's SMs (0 on failure)
@@ -637,6 +644,29 @@ inline bool make_planes(Planes &m, const void *w, uint64_t rows, uint32_t K) {
          wc12l::make_map(&m.lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, p + L.off_lo, K, rows, K, kUnit, kSubRows,
                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
+
+// What a device's set-up gave (0: failed), once per device, and again in a
+// context created afresh (the kernels' attributes must be set again then).
+class DeviceSetup {
+ public:
+  template <class F>
+  int get(F setup) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu_);
+    const unsigned long long ctx = wc::current_context_id();
+    if (value_[dev] == 0 || ctx == 0 || ctx_[dev] != ctx) {
+      value_[dev] = setup();
+      ctx_[dev] = wc::current_context_id();  // the set-up made the device's context current
+    }
+    return value_[dev];
+  }
+
+ private:
+  std::mutex mu_;
+  int value_[64] = {};
+  unsigned long long ctx_[64] = {};
+};
 
 // Launches a kernel in clusters of `cluster` CTAs along x; dependent: it may start while the kernel before it in the stream runs
 // (it waits with wait_prerequisites).

@@ -7,7 +7,6 @@ CPU path: if libwc.so is missing or no CUDA device is present the calls fail.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -603,36 +602,44 @@ def check_status(status: torch.Tensor, what: str = "device status") -> None:
     _check(int(status.item()), what)
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _on(device: torch.device, stream):
-    """The context to launch and allocate in: the device and the stream."""
+def _elsewhere(device: torch.device, stream):
+    """The context to allocate and launch in, or None where that is the
+    current one: the tensors' device, the stream given."""
     if stream is not None:
         if stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if torch._C._cuda_getDevice() != device.index:
         return torch.cuda.device(device)
-    return _NO_CONTEXT
+    return None
+
+
+def _bad(name: str, t, dtype, shape, device):
+    """Raises what is wrong with an argument that is not such a tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the container's device, {device}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
 def _want(name: str, t, dtype, shape, device) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{name} must be a tensor of {dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on the container's CUDA device")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    return t
+    """The tensor, contiguous, if it is what the call takes."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device:
+        _bad(name, t, dtype, shape, device)
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _container(name: str, t: torch.Tensor) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous():
+def _container(name: str, t) -> torch.device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a 1-D contiguous uint8 tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return t
+    return t.device
 
 
 def _status_word(status, device) -> torch.Tensor:
@@ -640,13 +647,16 @@ def _status_word(status, device) -> torch.Tensor:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("a captured call needs a status word of the caller's")
         return torch.zeros(1, dtype=torch.int32, device=device)
-    return _want("status", status, torch.int32, (1,), device)
+    if not isinstance(status, torch.Tensor) or status.dtype is not torch.int32 or status.numel() != 1 or status.device != device:
+        _bad("status", status, torch.int32, (1,), device)
+    return status
 
 
 def _output(out, shape, dtype, device) -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _want("out", out, dtype, tuple(shape), device)
+    if not isinstance(out, torch.Tensor) or out.dtype is not dtype or out.shape != shape or out.device != device:
+        _bad("out", out, dtype, shape, device)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     return out
@@ -657,19 +667,22 @@ def split12_embed(cont: torch.Tensor, V: int, K: int, ids: torch.Tensor, scale: 
     """scale * table[ids] (bf16, or fp32) with the V x K bf16 table given as a
     Split12 container on the device (wc12_embed); ids int32 or int64 of any
     shape.  An id outside [0, V) gives a row of zeros and an error."""
-    dev = _container("cont", cont).device
-    _want("ids", ids, (torch.int64, torch.int32), None, dev)
+    dev = _container("cont", cont)
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return split12_embed(cont, V, K, ids, scale, dtype, out, status)
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int64, torch.int32):
+        raise TypeError("ids must be a tensor of int32 or int64")
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("the output is bf16 or fp32")
-    with _on(dev, stream):
-        ids = ids.contiguous()
-        y = _output(out, (*ids.shape, K), dtype, dev)
-        st = _status_word(status, dev)
-        _check(load().wc12_embed(cont.data_ptr(), cont.numel(), V, K, ids.data_ptr(), ids.element_size(),
-                                 ids.numel(), scale, y.data_ptr(), _DT[dtype], st.data_ptr(), _stream(None)),
-               "wc12_embed")
-        if status is None:
-            check_status(st, "wc12_embed (device status)")
+    ids = _want("ids", ids, ids.dtype, ids.shape, dev)
+    y = _output(out, (*ids.shape, K), dtype, dev)
+    st = _status_word(status, dev)
+    _check((_lib or load()).wc12_embed(cont.data_ptr(), cont.numel(), V, K, ids.data_ptr(), ids.element_size(), ids.numel(),
+                                       scale, y.data_ptr(), _DT[dtype], st.data_ptr(), _raw_stream(dev)), "wc12_embed")
+    if status is None:
+        check_status(st, "wc12_embed (device status)")
     return y
 
 
@@ -680,31 +693,33 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     none), with W (N x K bf16) given as a Split12 container on the device
     (wc12_linear_adapters): x M x K bf16, a L x r x K and b L x N x r bf16,
     scales L fp32.  The plan serves batches of more than 16 tokens."""
-    dev = _container("cont", cont).device
+    dev = _container("cont", cont)
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return split12_linear_adapters(cont, N, K, x, adapter, a, b, scales, plan, out, status)
     if x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be M x K and a L x r x K")
     M, (L, r, _k) = x.shape[0], a.shape
-    _want("x", x, torch.bfloat16, (M, K), dev)
-    _want("adapter", adapter, torch.int32, (M,), dev)
-    _want("a", a, torch.bfloat16, (L, r, K), dev)
-    _want("b", b, torch.bfloat16, (L, N, r), dev)
-    _want("scales", scales, torch.float32, (L,), dev)
+    x = _want("x", x, torch.bfloat16, (M, K), dev)
+    adapter = _want("adapter", adapter, torch.int32, (M,), dev)
+    a = _want("a", a, torch.bfloat16, (L, r, K), dev)
+    b = _want("b", b, torch.bfloat16, (L, N, r), dev)
+    scales = _want("scales", scales, torch.float32, (L,), dev)
+    plan_ptr = plan_bytes = 0
     if plan is not None:
-        _container("plan", plan)
-        _want("plan", plan, torch.uint8, None, dev)
-    lib = load()
-    with _on(dev, stream):
-        x, adapter, a, b, scales = (t.contiguous() for t in (x, adapter, a, b, scales))
-        y = _output(out, (M, N), torch.float32, dev)
-        st = _status_word(status, dev)
-        work = torch.empty(M * r, dtype=torch.float32, device=dev)
-        _check(lib.wc12_linear_adapters(cont.data_ptr(), cont.numel(), None if plan is None else plan.data_ptr(),
-                                        0 if plan is None else plan.numel(), N, K, x.data_ptr(), M,
-                                        adapter.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), L, r,
-                                        y.data_ptr(), work.data_ptr(), 4 * work.numel(), st.data_ptr(),
-                                        _stream(None)), "wc12_linear_adapters")
-        if status is None:
-            check_status(st, "wc12_linear_adapters (device status)")
+        if _container("plan", plan) != dev:
+            raise ValueError(f"plan must be on the container's device, {dev}")
+        plan_ptr, plan_bytes = plan.data_ptr(), plan.numel()
+    y = _output(out, (M, N), torch.float32, dev)
+    st = _status_word(status, dev)
+    work = torch.empty(M * r, dtype=torch.float32, device=dev)
+    _check((_lib or load()).wc12_linear_adapters(
+        cont.data_ptr(), cont.numel(), plan_ptr or None, plan_bytes, N, K, x.data_ptr(), M, adapter.data_ptr(), a.data_ptr(),
+        b.data_ptr(), scales.data_ptr(), L, r, y.data_ptr(), work.data_ptr(), 4 * M * r, st.data_ptr(), _raw_stream(dev)),
+        "wc12_linear_adapters")
+    if status is None:
+        check_status(st, "wc12_linear_adapters (device status)")
     return y
 
 
@@ -716,28 +731,30 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
     two Split12 containers on the device, gate_up E x 2F x H and down
     E x H x F (wc12_moe): the k experts with the largest logits, their softmax
     (over themselves, or without renormalize over all experts), SiLU-gated."""
-    dev = _container("gate_up", gate_up).device
-    _container("down", down)
-    _want("down", down, torch.uint8, None, dev)
+    dev = _container("gate_up", gate_up)
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return split12_moe(gate_up, down, E, H, F, x, logits, k, renormalize, dtype, out, status)
+    if _container("down", down) != dev:
+        raise ValueError(f"down must be on the container's device, {dev}")
     if x.dim() != 2:
         raise ValueError("x must be T x H")
     T = x.shape[0]
-    _want("x", x, torch.bfloat16, (T, H), dev)
-    _want("logits", logits, torch.float32, (T, E), dev)
+    x = _want("x", x, torch.bfloat16, (T, H), dev)
+    logits = _want("logits", logits, torch.float32, (T, E), dev)
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("the output is bf16 or fp32")
-    lib = load()
-    with _on(dev, stream):
-        x, logits = x.contiguous(), logits.contiguous()
-        y = _output(out, (T, H), dtype, dev)
-        st = _status_word(status, dev)
-        work = torch.empty(lib.wc12_moe_work_bytes(T, k, F), dtype=torch.uint8, device=dev)
-        _check(lib.wc12_moe(gate_up.data_ptr(), gate_up.numel(), down.data_ptr(), down.numel(), E, H, F,
-                            x.data_ptr(), logits.data_ptr(), T, k, 1 if renormalize else 0, y.data_ptr(),
-                            _DT[dtype], work.data_ptr(), work.numel(), st.data_ptr(), _stream(None)),
-               "wc12_moe")
-        if status is None:
-            check_status(st, "wc12_moe (device status)")
+    lib = _lib or load()
+    y = _output(out, (T, H), dtype, dev)
+    st = _status_word(status, dev)
+    work_bytes = lib.wc12_moe_work_bytes(T, k, F)
+    work = torch.empty(work_bytes, dtype=torch.uint8, device=dev)
+    _check(lib.wc12_moe(gate_up.data_ptr(), gate_up.numel(), down.data_ptr(), down.numel(), E, H, F, x.data_ptr(),
+                        logits.data_ptr(), T, k, 1 if renormalize else 0, y.data_ptr(), _DT[dtype], work.data_ptr(), work_bytes,
+                        st.data_ptr(), _raw_stream(dev)), "wc12_moe")
+    if status is None:
+        check_status(st, "wc12_moe (device status)")
     return y
 
 
