@@ -42,7 +42,7 @@ struct Params {
   const int32_t *adapter;  // [M]
   const uint16_t *a, *b;   // [L, r, K], [L, N, r]
   const float *scale;      // [L]
-  float *t;                // [M, r]
+  float *t;                // [M, r], or three planes of bf16
   float *y;                // [M, N]
   uint32_t M, N, K, r, L;
   int32_t *status;
@@ -60,73 +60,129 @@ __device__ __forceinline__ void split3(float v, uint32_t &h0, uint32_t &h1, uint
   h2 = __float_as_uint(r1 - __uint_as_float(h1)) & 0xFFFF0000u;
 }
 
+// loads that stay where they are written: all of a batch before its first use
+__device__ __forceinline__ uint4 load16(const uint16_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load8(const uint16_t *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 // ---------------------------------------------------------------------------
-// t[m][j] = s_a sum_k x[m][k] A_a[j][k].  A cluster takes 8 tokens (x), 16
-// ranks (y) and one adapter: that of token z of the 8, if it is the first
-// with it.  The warps of its CTAs split K, 64 values at a time (16 a lane, as
-// in wc12_few.cuh, A's rows in the place of the weights').
-__global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_constant__ Params p, uint32_t csize) {
-  launch_dependents();
-  __shared__ float red[kSideWarps][8 * kRedTok];
-  __shared__ float part[128];
+// one adapter's part: the tokens `same` of the 8 kTiles from m0 on
+template <int kTiles>
+__device__ __forceinline__ void shrink_one(const Params &p, uint32_t csize, uint32_t rank, uint32_t m0, uint32_t j0, int32_t mine,
+                                           uint32_t same, float (*red)[8 * kTiles * kRedTok], float *part) {
+  constexpr int kTokens = 8 * kTiles, kBatch = kTiles == 1 ? 4 : 2;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = blockIdx.x % csize, m0 = 8 * (blockIdx.x / csize), j0 = 16 * blockIdx.y, z = blockIdx.z;
+  // ranks and tokens that do not exist are read as the last ones: their sums
+  // are dropped, and the loads need no condition
+  const uint32_t ra = j0 + g < p.r ? j0 + g : p.r - 1, rb = j0 + g + 8 < p.r ? j0 + g + 8 : p.r - 1;
+  const uint16_t *pa = p.a + (uint64_t(mine) * p.r + ra) * p.K + 16 * t, *pb = p.a + (uint64_t(mine) * p.r + rb) * p.K + 16 * t;
+  const uint16_t *px[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; i++) {
+    const uint32_t m = m0 + 8 * i + g;
+    px[i] = p.x + uint64_t(m < p.M ? m : p.M - 1) * p.K + 16 * t;
+  }
+  float tot[kTiles][4] = {};
+  const uint32_t step = 64 * kSideWarps * csize;
+  for (uint32_t k0 = 64 * (rank * kSideWarps + warp); k0 < p.K; k0 += kBatch * step) {
+    uint4 a0[kBatch][2], a1[kBatch][2], xv[kBatch][kTiles][2];
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      const uint32_t k = k0 + b * step < p.K ? k0 + b * step : k0;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        a0[b][h] = load16(pa + k + 8 * h);
+        a1[b][h] = load16(pb + k + 8 * h);
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) xv[b][i][h] = load16(px[i] + k + 8 * h);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      if (k0 + b * step >= p.K) break;
+#pragma unroll
+      for (int i = 0; i < kTiles; i++) {
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint32_t u0[4] = {a0[b][h].x, a1[b][h].x, a0[b][h].y, a1[b][h].y}, u1[4] = {a0[b][h].z, a1[b][h].z, a0[b][h].w, a1[b][h].w};
+          mma(d, u0, xv[b][i][h].x, xv[b][i][h].y);
+          mma(d, u1, xv[b][i][h].z, xv[b][i][h].w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) tot[i][j] += d[j];
+      }
+    }
+  }
+  put_sums<kTiles>(red[warp], tot, lane);
+  __syncthreads();
+  for (uint32_t o = tid; o < kTokens * 16; o += kSideThreads) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSideWarps; w++) sum += red[w][(o >> 4) * kRedTok + (o & 15)];
+    part[o] = sum;
+  }
+  if (csize > 1) cluster_sync(); else __syncthreads();
+  for (uint32_t o = tid + rank * kSideThreads; o < kTokens * 16; o += kSideThreads * csize) {
+    const uint32_t j = o & 15, m = o >> 4;
+    if (!((same >> m) & 1u) || j0 + j >= p.r) continue;
+    float sum = part[o];
+    if (csize > 1) {
+      sum = 0.0f;
+      for (uint32_t c = 0; c < csize; c++) sum += cluster_load(&part[o], c);
+    }
+    sum *= p.scale[mine];
+    const uint64_t at = uint64_t(m0 + m) * p.r + j0 + j;
+    if (kTiles == 1) {
+      p.t[at] = sum;
+    } else {
+      uint32_t h0, h1, h2;
+      split3(sum, h0, h1, h2);
+      uint16_t *q = reinterpret_cast<uint16_t *>(p.t) + at;
+      const uint64_t plane = uint64_t(p.M) * p.r;
+      q[0] = uint16_t(h0 >> 16);
+      q[plane] = uint16_t(h1 >> 16);
+      q[2 * plane] = uint16_t(h2 >> 16);
+    }
+  }
+  if (csize > 1) cluster_sync(); else __syncthreads();  // the sums are read until here
+}
+
+// t[m][j] = s_a sum_k x[m][k] A_a[j][k].  A cluster takes 8 kTiles tokens (x),
+// 16 ranks (y) and, of the adapters that its tokens have, the z-th and every
+// gridDim.z-th one after it.  The warps of its CTAs split K, 64 values at a
+// time (16 a lane, as in wc12_few.cuh, A's rows in the place of the
+// weights'), kBatch of them in flight.  With 8 tokens t is written in fp32, with 32 (which the
+// tensor-core product of t and B follows) as three planes of bf16.
+template <int kTiles>
+__global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_constant__ Params p, uint32_t csize) {
+  constexpr int kTokens = 8 * kTiles;
+  launch_dependents();
+  __shared__ float red[kSideWarps][kTokens * kRedTok];
+  __shared__ float part[kTokens * 16];
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % csize, m0 = kTokens * (blockIdx.x / csize), j0 = 16 * blockIdx.y, z = blockIdx.z;
   int32_t ad = -1;
-  if (lane < 8 && m0 + lane < p.M) ad = p.adapter[m0 + lane];
+  if (lane < kTokens && m0 + lane < p.M) ad = p.adapter[m0 + lane];
   if (ad < -1 || ad >= int32_t(p.L)) {
     report(p.status, WC_ERR_INVALID_ARG);
     ad = -1;
   }
-  const int32_t mine = __shfl_sync(0xffffffffu, ad, z);
-  const uint32_t same = __ballot_sync(0xffffffffu, lane < 8 && ad == mine);
-  if (mine < 0 || (same & ((1u << z) - 1u)) != 0) return;  // the whole cluster
-  const bool live = (same >> g) & 1u;
-  const uint16_t *px = p.x + uint64_t(m0 + g) * p.K + 16 * t;
-  const bool r0 = j0 + g < p.r, r1 = j0 + g + 8 < p.r;
-  const uint16_t *pa = p.a + (uint64_t(mine) * p.r + j0 + g) * p.K + 16 * t;
-  float tot[1][4] = {};
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 4
-  for (uint32_t k = 64 * (rank * kSideWarps + warp); k < p.K; k += 64 * kSideWarps * csize) {
-    uint4 a0[2] = {zero, zero}, a1[2] = {zero, zero}, xv[2] = {zero, zero};
-    if (r0) {
-      a0[0] = *reinterpret_cast<const uint4 *>(pa + k);
-      a0[1] = *reinterpret_cast<const uint4 *>(pa + k + 8);
-    }
-    if (r1) {
-      a1[0] = *reinterpret_cast<const uint4 *>(pa + uint64_t(8) * p.K + k);
-      a1[1] = *reinterpret_cast<const uint4 *>(pa + uint64_t(8) * p.K + k + 8);
-    }
-    if (live) {
-      xv[0] = *reinterpret_cast<const uint4 *>(px + k);
-      xv[1] = *reinterpret_cast<const uint4 *>(px + k + 8);
-    }
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const uint32_t u0[4] = {a0[h].x, a1[h].x, a0[h].y, a1[h].y}, u1[4] = {a0[h].z, a1[h].z, a0[h].w, a1[h].w};
-      mma(d, u0, xv[h].x, xv[h].y);
-      mma(d, u1, xv[h].z, xv[h].w);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) tot[0][i] += d[i];
+  // tokens that are the first with their adapter
+  const uint32_t with_it = __match_any_sync(0xffffffffu, ad);  // every lane, before any condition
+  uint32_t rest = __ballot_sync(0xffffffffu, ad >= 0 && uint32_t(__ffs(with_it) - 1) == lane);
+  for (uint32_t i = 0; rest; rest &= rest - 1, i++) {
+    if (i % gridDim.z != z) continue;
+    const int32_t mine = __shfl_sync(0xffffffffu, ad, __ffs(rest) - 1);
+    shrink_one<kTiles>(p, csize, rank, m0, j0, mine, __ballot_sync(0xffffffffu, ad == mine), red, part);
   }
-  put_sums<1>(red[warp], tot, lane);
-  __syncthreads();
-  const uint32_t j = tid & 15, m = tid >> 4;
-  float sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kSideWarps; w++) sum += red[w][m * kRedTok + j];
-  if (csize > 1) {
-    part[tid] = sum;
-    cluster_sync();
-    if (rank == 0) {
-      sum = 0.0f;
-      for (uint32_t c = 0; c < csize; c++) sum += cluster_load(&part[tid], c);
-    }
-    cluster_sync();  // the others' sums are read until here
-  }
-  if (rank == 0 && ((same >> m) & 1u) && j0 + j < p.r) p.t[uint64_t(m0 + m) * p.r + j0 + j] = p.scale[mine] * sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -137,8 +193,8 @@ struct Few {
   static constexpr uint32_t kXBox = NT * 1024;  // 8 NT tokens' values of a unit
   static constexpr uint32_t kStage = 2 * kSubBytes + 2 * kXBox;
   static constexpr uint32_t kOwn = own_words(8 * NT);  // words of a warp: its list, then its sums
-  static constexpr uint32_t kLists = kDepth * kStage;
-  static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
+  static constexpr uint32_t kQueues = kDepth * kStage;
+  static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = 1024 + kBars + sizeof(Bars);  // 1024: the boxes' swizzle counts from there
 };
 
@@ -159,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
   if (tid == 0) bars_init(bars);
   __syncthreads();
   bool ok;
-  float *red = reinterpret_cast<float *>(dyn + F::kLists);
+  float *red = reinterpret_cast<float *>(dyn + F::kQueues);
   if (warp == kWarps) {
     Turn turn;
     auto load = [&](uint32_t u) {
@@ -193,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
     Window win;
     window_offsets(win, v.exc_off, row0, K, lane);
     Exceptions x;
-    x.list = reinterpret_cast<uint32_t *>(dyn + F::kLists) + warp * F::kOwn;
-    exceptions_reset(x);
+    x.q = reinterpret_cast<Queues *>(dyn + F::kQueues + warp * F::kOwn * 4);
+    exceptions_reset(x, lane);
     ok = open_header(v, p.w, p.w_bytes);
     float tot0[NT][4] = {}, tot1[NT][4] = {};
     if (ok) {
@@ -206,14 +262,14 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
       const XAt xat = x_boxes(lane);
       Turn turn;
       for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
-        Handed h;
-        const uint32_t most = exceptions_hand(x, h, u, lane);
+        const uint32_t most = exceptions_most(x, u, lane);
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
         const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
         const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == u1, u, u, u + 1, row0, row0};
-        if (most == 1) stage_product<NT, 1, false, false>(tot0, tot1, at, xat, v.book, h, lane);
-        else if (most == 2) stage_product<NT, 1, false, true>(tot0, tot1, at, xat, v.book, h, lane);
+        if (most == 1) stage_product<NT, 1, false, false>(tot0, tot1, at, xat, v.book, x, lane);
+        else if (most == 2) stage_product<NT, 1, false, true>(tot0, tot1, at, xat, v.book, x, lane);
         else stage_product_slow<NT, 1, false>(tot0, tot1, at, xat, v, x, K, lane);
+        exceptions_pass(x, at.key, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
@@ -311,65 +367,73 @@ int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // More tokens: Y = the adapters' part (zero for a token without one).  A warp
 // takes 16 rows of N and 32 tokens; t enters as three bf16 numbers.
-__global__ void __launch_bounds__(kSideThreads) k12_adapter_expand(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __grid_constant__ Params p) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t n0 = (blockIdx.y * kSideWarps + warp) * kRows, m0 = 32 * blockIdx.x;
-  int32_t ad = -1;
-  if (m0 + lane < p.M) ad = p.adapter[m0 + lane];
+  int32_t ad = m0 + lane < p.M ? p.adapter[m0 + lane] : -1;
   if (ad < 0 || ad >= int32_t(p.L)) ad = -1;
-  float d[4][4] = {};
+  const uint64_t plane = uint64_t(p.M) * p.r;
+  const uint16_t *pt[4];  // tokens that do not exist are read as the last one, and dropped
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t m = m0 + 8 * i + g;
+    pt[i] = reinterpret_cast<const uint16_t *>(p.t) + uint64_t(m < p.M ? m : p.M - 1) * p.r + 4 * t;
+  }
+  // a token's part goes to Y as its adapter's turn comes: another adapter's
+  // infinite values never meet it
+  auto put = [&](const float (*c)[4], uint32_t tokens) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t m = 8 * i + 2 * t + (j & 1);
+        if ((tokens >> m) & 1u) p.y[uint64_t(m0 + m) * p.N + n0 + g + 8 * (j >> 1)] = c[i][j];
+      }
+  };
   wait_prerequisites();
   uint32_t rest = __ballot_sync(0xffffffffu, ad >= 0);
+  const uint32_t exist = __ballot_sync(0xffffffffu, m0 + lane < p.M);
+  if (exist & ~rest) {
+    const float zero[4][4] = {};
+    put(zero, exist & ~rest);
+  }
   while (rest) {
     const int32_t cur = __shfl_sync(0xffffffffu, ad, __ffs(rest) - 1);
     const uint32_t same = __ballot_sync(0xffffffffu, ad == cur);
     rest &= ~same;
     const uint16_t *pb = p.b + (uint64_t(cur) * p.N + n0 + g) * p.r + 4 * t;
     float c[4][4] = {};
+#pragma unroll 1
     for (uint32_t j = 0; j < p.r; j += 16) {
-      uint2 b0 = make_uint2(0u, 0u), b1 = b0;
       const bool in = j + 4 * t < p.r;
-      if (in) {
-        b0 = *reinterpret_cast<const uint2 *>(pb + j);
-        b1 = *reinterpret_cast<const uint2 *>(pb + uint64_t(8) * p.r + j);
+      const uint32_t k = in ? j : 0;
+      uint2 b0 = load8(pb + k), b1 = load8(pb + uint64_t(8) * p.r + k), v[4][3];
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int part = 0; part < 3; part++) v[i][part] = load8(pt[i] + k + part * plane);
+      if (!in) {  // ranks past the last, in the last step of a rank that is no multiple of 16
+        b0 = b1 = make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int part = 0; part < 3; part++) v[i][part] = make_uint2(0u, 0u);
       }
       const uint32_t a[4] = {b0.x, b1.x, b0.y, b1.y};
 #pragma unroll
-      for (int nt = 0; nt < 4; nt++) {
-        if (((same >> (8 * nt)) & 0xFFu) == 0) continue;
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in && ((same >> (8 * nt + g)) & 1u))
-          q = *reinterpret_cast<const float4 *>(p.t + uint64_t(m0 + 8 * nt + g) * p.r + j + 4 * t);
-        uint32_t h[4][3];
-        split3(q.x, h[0][0], h[0][1], h[0][2]);
-        split3(q.y, h[1][0], h[1][1], h[1][2]);
-        split3(q.z, h[2][0], h[2][1], h[2][2]);
-        split3(q.w, h[3][0], h[3][1], h[3][2]);
+      for (int part = 2; part >= 0; part--)
 #pragma unroll
-        for (int part = 2; part >= 0; part--)
-          mma(c[nt], a, (h[0][part] >> 16) | h[1][part], (h[2][part] >> 16) | h[3][part]);
-      }
+        for (int i = 0; i < 4; i++) mma(c[i], a, v[i][part].x, v[i][part].y);
     }
-    // to this adapter's tokens only: another's zeros times an infinite value
-    // of B would be NaN
-#pragma unroll
-    for (int nt = 0; nt < 4; nt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if ((same >> (8 * nt + 2 * t + (i & 1))) & 1u) d[nt][i] = c[nt][i];
+    put(c, same);
   }
-#pragma unroll
-  for (int nt = 0; nt < 4; nt++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t m = m0 + 8 * nt + 2 * t + (i & 1), row = n0 + g + 8 * (i >> 1);
-      if (m < p.M) p.y[uint64_t(m) * p.N + row] = d[nt][i];
-    }
 }
 
 }  // namespace wc12a
 
-extern "C" uint64_t wc12_linear_adapters_work_bytes(uint32_t M, uint32_t r) { return uint64_t(M) * r * 4; }
+extern "C" uint64_t wc12_linear_adapters_work_bytes(uint32_t M, uint32_t r) {
+  return uint64_t(M) * r * (M <= wc12a::kFewTokens ? 4 : 6);
+}
 
 extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes,
                                         uint32_t N, uint32_t K, const void *d_x, uint32_t M, const int32_t *d_adapter,
@@ -407,10 +471,14 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   p.status = d_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
-    const uint32_t tiles = (M + 7) / 8, ranks = (r + 15) / 16, z = M < 8 ? M : 8;
-    uint32_t csize = 1;  // CTAs that split K: until each SM has two, while a warp has two pieces
+    const uint32_t tokens = M <= kFewTokens ? 8 : 32, tiles = (M + tokens - 1) / tokens, ranks = (r + 15) / 16;
+    // the tokens' adapters side by side, and CTAs that split K, until each
+    // SM has some CTAs (while a warp has two pieces)
+    uint32_t z = 1, csize = 1;
+    while (z < tokens && z < M && tiles * ranks * z < 2u * uint32_t(sms)) z *= 2;
     while (csize < 8 && tiles * ranks * csize < 2u * uint32_t(sms) && K / 64 >= 4 * csize * kSideWarps) csize *= 2;
-    if (launch(k12_adapter_shrink, dim3(tiles * csize, ranks, z), kSideThreads, csize, 0, s, false, p, csize) != cudaSuccess)
+    if (launch(M <= kFewTokens ? k12_adapter_shrink<1> : k12_adapter_shrink<4>, dim3(tiles * csize, ranks, z), kSideThreads, csize, 0, s,
+               false, p, csize) != cudaSuccess)
       return WC_ERR_CUDA;
   }
   if (M <= kFewTokens) return M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s);

@@ -44,7 +44,7 @@ struct Route {
   uint16_t pair[kMaxPairs];  // token * k + j, by expert
   uint16_t item_e[kMaxPairs], item_first[kMaxPairs];
   uint8_t item_n[kMaxPairs];
-  uint32_t items, pairs;
+  uint32_t items;
 };
 struct Params {
   const uint8_t *gate_up, *down;
@@ -147,10 +147,7 @@ __global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_co
       pairs += both & 0xFFFFu;
       items += both >> 16;
     }
-    if (lane == 0) {
-      r.items = items;
-      r.pairs = pairs;
-    }
+    if (lane == 0) r.items = items;
   }
   __syncthreads();
   // by token within an expert
@@ -162,22 +159,21 @@ __global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_co
 }
 
 // The route, as the two products have it: from the workspace into shared
-// memory, what there is of it (every thread; a barrier has to follow).
-__device__ __forceinline__ void take_route(Route &r, const Route *from) {
-  const uint32_t tid = threadIdx.x, items = from->items, pairs = from->pairs;
-  for (uint32_t i = tid; i < items; i += kThreads) {
-    r.item_e[i] = from->item_e[i];
-    r.item_first[i] = from->item_first[i];
-    r.item_n[i] = from->item_n[i];
+// memory (every thread; a barrier has to follow).  As much as there can be of
+// it is copied, not as much as there is, which would have to be read first.
+__device__ __forceinline__ void take_route(Route &r, const Route *from, uint32_t most) {
+  const uint32_t tid = threadIdx.x;
+  for (uint32_t i = tid; i < most; i += kThreads) {
+    const float weight = from->weight[i];
+    const uint16_t pair = from->pair[i], e = from->item_e[i], first = from->item_first[i];
+    const uint8_t n = from->item_n[i];
+    r.weight[i] = weight;
+    r.pair[i] = pair;
+    r.item_e[i] = e;
+    r.item_first[i] = first;
+    r.item_n[i] = n;
   }
-  for (uint32_t i = tid; i < pairs; i += kThreads) {
-    r.pair[i] = from->pair[i];
-    r.weight[i] = from->weight[i];
-  }
-  if (tid == 0) {
-    r.items = items;
-    r.pairs = pairs;
-  }
+  if (tid == 0) r.items = from->items;
 }
 
 // ---------------------------------------------------------------------------
@@ -187,8 +183,8 @@ struct Up {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 8 * kXRow);
   static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its list, then its sums of G_e and U_e
   static constexpr uint32_t kRoute = kDepth * kStage;
-  static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
-  static constexpr uint32_t kBars = kLists + kWarps * kOwn * 4;
+  static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
+  static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = kBars + sizeof(Bars);
 };
 
@@ -215,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   if (tid == 0) bars_init(bars);
   wait_prerequisites();  // the route
   launch_dependents();   // the down product's CTAs, which read the route too
-  take_route(r, p.route);
+  take_route(r, p.route, p.T * p.k);
   __syncthreads();
   if (!ok) {
     if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
@@ -274,14 +270,14 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   offsets(next, first + clusters);
   entries(now, first);
   Exceptions x;
-  x.list = reinterpret_cast<uint32_t *>(dyn + Up::kLists) + warp * Up::kOwn;
-  float *sums = reinterpret_cast<float *>(dyn + Up::kLists);
+  x.q = reinterpret_cast<Queues *>(dyn + Up::kQueues + warp * Up::kOwn * 4);
+  float *sums = reinterpret_cast<float *>(dyn + Up::kQueues);
   const uint64_t plane = uint64_t(p.T) * p.k * p.F;
   const XAt xat = x_rows(lane);
   const uint32_t g = lane >> 2, t = lane & 3;
   bool alive = true;
   for (uint32_t job = first; job < jobs; job += clusters) {
-    exceptions_reset(x);
+    exceptions_reset(x, lane);
     if (v.ne > 0) {
 #pragma unroll 1
       for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
@@ -293,15 +289,15 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
     offsets(next, job + 2 * clusters);
     float gate[1][4] = {}, up[1][4] = {};
     for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
-      Handed h;
-      const uint32_t most = exceptions_hand(x, h, 2 * u, lane);
+      const uint32_t most = exceptions_most(x, 2 * u, lane);
       alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
       const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
-      if (most == 1) stage_product<1, 1, true, false>(gate, up, at, xat, v.book, h, lane);
-      else if (most == 2) stage_product<1, 1, true, true>(gate, up, at, xat, v.book, h, lane);
+      if (most == 1) stage_product<1, 1, true, false>(gate, up, at, xat, v.book, x, lane);
+      else if (most == 2) stage_product<1, 1, true, true>(gate, up, at, xat, v.book, x, lane);
       else stage_product_slow<1, 1, true>(gate, up, at, xat, v, x, K, lane);
+      exceptions_pass(x, at.key, lane);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
@@ -341,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
 struct Down {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 16 * kXRow);
   static constexpr uint32_t kRoute = kDepth * kStage;
-  static constexpr uint32_t kLists = align128(kRoute + uint32_t(sizeof(Route)));
-  static constexpr uint32_t kBars = kLists + kWarps * kListCap * 4;
+  static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
+  static constexpr uint32_t kBars = kQueues + kWarps * uint32_t(sizeof(Queues));
   static constexpr uint32_t kAcc = align128(kBars + uint32_t(sizeof(Bars)));
   static __host__ __device__ uint32_t smem(uint32_t T) { return kAcc + kWarps * T * kRedTok * 4; }
 };
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
   if (warp < kWarps)
     for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
-  take_route(r, p.route);  // the up product's CTAs had it before this one could start
+  take_route(r, p.route, p.T * p.k);  // the up product's CTAs had it before this one could start
   __syncthreads();
   // the items' stages one after another; this CTA's: [q0, q1)
   const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2, all = r.items * per, ring = smem_u32(dyn);
@@ -434,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
     offsets(next, first + 1);
     entries(now, first);
     Exceptions x;
-    x.list = reinterpret_cast<uint32_t *>(dyn + Down::kLists) + warp * kListCap;
+    x.q = reinterpret_cast<Queues *>(dyn + Down::kQueues + warp * sizeof(Queues));
     const XAt xat = x_rows(lane);
     uint32_t st = st0;
     bool alive = true;
     for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
       const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
-      exceptions_reset(x);
+      exceptions_reset(x, lane);
       if (v.ne > 0) {
         window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
         exceptions_ready(x, lane);
@@ -450,15 +446,15 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       offsets(next, item + 2);
       float tot0[1][4] = {}, tot1[1][4] = {};
       for (; st < end; st++, q++, turn.next()) {
-        Handed h;
-        const uint32_t most = exceptions_hand(x, h, 2 * st, lane);
+        const uint32_t most = exceptions_most(x, 2 * st, lane);
         alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
         if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
         const StageAt at{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row_of(item), row_of(item)};
-        if (most == 1) stage_product<1, 2, false, false>(tot0, tot1, at, xat, v.book, h, lane);
-        else if (most == 2) stage_product<1, 2, false, true>(tot0, tot1, at, xat, v.book, h, lane);
+        if (most == 1) stage_product<1, 2, false, false>(tot0, tot1, at, xat, v.book, x, lane);
+        else if (most == 2) stage_product<1, 2, false, true>(tot0, tot1, at, xat, v.book, x, lane);
         else stage_product_slow<1, 2, false>(tot0, tot1, at, xat, v, x, K, lane);
+        exceptions_pass(x, at.key, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
@@ -499,6 +495,7 @@ int up_slots() {
     int per_sm = 0;
     if (cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) != cudaSuccess ||
         cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
+        cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess)
       return 0;
     return per_sm * wc12l::device_sms();
@@ -563,7 +560,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     // down: CTAs that split the items, the same
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
     uint32_t cd = 1;
-    while (cd < 8 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
+    while (cd < 16 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||

@@ -31,11 +31,11 @@
 // before the product, so that an output has the exact weights and nothing
 // else in its sum.  A warp takes the exceptions of its 16 rows from the
 // container's per-chunk lists, 64 entries a load, while its first weights are
-// in flight (or the ones of the rows before), and keeps those of its part of
-// K, one a lane.  More than its list holds: it looks each lane's values up in
-// the container's sorted lists instead (slow, and right for any container).  A
-// stage's entries are handed to the lanes that hold their values before the
-// products, which then take them in passing, without a branch.
+// in flight (or the ones of the rows before), and gives those of its part of
+// K to the lanes that will hold their values, each of which has a short
+// queue.  The products take a lane's next entry in passing, without a branch.
+// More than a queue holds: each lane's values are looked up in the
+// container's sorted lists instead (slow, and right for any container).
 #pragma once
 
 #include <cstdint>
@@ -71,7 +71,7 @@ constexpr uint32_t kRows = 16;       // weight rows of a group
 constexpr uint32_t kSubRows = 64;    // of a subtile
 constexpr uint32_t kUnit = 64;       // values of K of a subtile
 constexpr uint32_t kMaxK = 1 << 16;  // a group's rows touch at most 17 chunks
-constexpr uint32_t kListCap = 256;   // exceptions a warp keeps
+constexpr uint32_t kQueue = 16;      // exceptions a lane keeps
 constexpr uint32_t kRedTok = 18;     // floats a token's 16 sums take (padded: few bank conflicts)
 constexpr uint32_t kDepth = 3;       // stages of the ring
 constexpr uint32_t kSpinLimit = 1u << 24;
@@ -187,8 +187,15 @@ __device__ __forceinline__ uint2 shared8(uint32_t a) {
   return v;
 }
 
-// A warp's own part of shared memory: its list of exceptions, then its sums.
-constexpr uint32_t own_words(uint32_t tokens) { return tokens * kRedTok > kListCap ? tokens * kRedTok : kListCap; }
+// A warp's own part of shared memory: its lanes' queues, then its sums.
+struct Queues {
+  uint32_t count[32];
+  uint16_t entry[kQueue][32];
+  uint8_t high[kQueue][32];
+};
+constexpr uint32_t own_words(uint32_t tokens) {
+  return tokens * kRedTok * 4 > sizeof(Queues) ? tokens * kRedTok : uint32_t(sizeof(Queues)) / 4;
+}
 
 __device__ __forceinline__ uint32_t shared4(uint32_t a) {
   uint32_t v;
@@ -321,23 +328,14 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // ---------------------------------------------------------------------------
-// Exceptions.  An entry: high byte (bits 0-7), row of the group (8-11),
-// column of the unit (12-17), key (18-31): which subtile of the warp's rows,
-// numbered as the warp meets them.
-constexpr uint32_t kExcKey = 18;
-__device__ __forceinline__ uint32_t pack_exc(uint32_t key, uint32_t col, uint32_t row, uint32_t high) {
-  return high | (row << 8) | (col << 12) | (key << kExcKey);
-}
-// An entry as its lane uses it: the place among the 16 sets of 4 values that
-// it has of a stage (8 subtile + 2 step + row half), and which of the 4.
-__device__ __forceinline__ uint32_t exc_owner(uint32_t e) { return ((e >> 8) & 7u) * 4 + ((e >> 16) & 3u); }
-__device__ __forceinline__ uint32_t exc_place(uint32_t e, uint32_t key) {
-  return (((e >> kExcKey) - key) << 3) | ((e >> 13) & 6u) | ((e >> 11) & 1u);
-}
-// selects the entry's byte in the place of value i of 4: prmt(hi4, e, ..)
-__device__ __forceinline__ uint32_t exc_select(uint32_t e) {
-  const uint32_t i = 4 * ((e >> 12) & 3u);
-  return (0x3210u & ~(0xFu << i)) | (4u << i);
+// Exceptions.  A lane's entry: which subtile, as the warp meets them (bits
+// 5-15), which of the lane's 8 sets of 4 values there (2 step + row half;
+// bits 2-4), which value of the set (0-1).
+constexpr uint32_t kNever = 0x7FFFFFFFu;  // the set of no entry
+// the byte `high` (in bits 16-23) into place `entry` & 3 of four
+__device__ __forceinline__ uint32_t put_high(uint32_t hi4, uint32_t entry) {
+  const uint32_t i = 4 * (entry & 3u);
+  return prmt(hi4, entry, (0x3210u & ~(0xFu << i)) | (6u << i));
 }
 
 // The container's exceptions around a group of 16 rows, in flight: lane j
@@ -369,11 +367,13 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
   window_pairs(v, (e0 & ~uint64_t(1)) + 2 * lane, e1 <= v.ne ? e1 : 0, w.pos, w.val);
 }
 
-// What a warp keeps of its exceptions: cnt entries in `list`, the lane's one
-// of the first 32 in e; walk: too many, look them up.
+// A lane's exceptions: its queue of n entries, ascending, of which the next
+// two are out, as their set (entry >> 2) and the entry with its high byte in
+// bits 16-23.  walk (the same for the warp): too many, look them up.
 struct Exceptions {
-  uint32_t *list;
-  uint32_t cnt, e;
+  Queues *q;
+  uint32_t n, i;  // entries, and the first that is not out
+  uint32_t set1, entry1, set2, entry2;
   bool walk;
 };
 // Entries have come: keeps those of the group's units [u0, u1), as of
@@ -386,7 +386,7 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
     if (lane == 0) report(status, WC_ERR_CORRUPT);
     return;
   }
-  if (e1 - e0 > 64 * kListCap) x.walk = true;
+  if (e1 - e0 > 1u << 14) x.walk = true;
   if (x.walk) return;
   const uint64_t f0 = row0 * K, c0 = f0 / kChunk;
   const uint32_t chunks = window_chunks(row0, K), count = uint32_t(e1 - e0), skew = uint32_t(e0 & 1);
@@ -411,43 +411,70 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
       // off by less than 2^-19
       const uint32_t row = uint32_t((float(lf) + 0.5f) * inv), col = lf - row * K, u = col / kUnit;
       in = in && u >= u0 && u < u1;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      if (x.cnt + __popc(m) > kListCap) {
-        x.walk = true;
-        return;
+      if (in) {
+        const uint32_t owner = (row & 7u) * 4 + ((col >> 4) & 3u), at = atomicAdd(&x.q->count[owner], 1u);
+        if (at < kQueue) {
+          x.q->entry[at][owner] = uint16_t((mul * u + plus) << 5 | ((col >> 2) & 3u) << 3 | (row >> 3) << 2 | (col & 3u));
+          x.q->high[at][owner] = uint8_t(val >> (8 * i));
+        }
       }
-      if (in) x.list[x.cnt + __popc(m & ((1u << lane) - 1u))] = pack_exc(mul * u + plus, col % kUnit, row, (val >> (8 * i)) & 0xFFu);
-      x.cnt += __popc(m);
     }
   }
 }
-// A stage's exceptions (subtiles key and key + 1), handed to their lanes: the
-// first of a lane, and the second, is e and select at place (16: none).
-// Returns 1, or if a lane has two 2, or if one has more (or walk) 3.
-struct Handed {
-  uint32_t place, e, select, place2, e2;
-};
-__device__ __forceinline__ uint32_t exceptions_hand(const Exceptions &x, Handed &h, uint32_t key, uint32_t lane) {
-  h.place = h.place2 = 16;
-  h.e = h.select = h.e2 = 0;
-  uint32_t most = x.walk ? 3 : 0;
-  auto hand = [&](uint32_t own, bool in) {
-    uint32_t hit = __ballot_sync(0xffffffffu, in && (own >> kExcKey) - key < 2);
-    for (; hit; hit &= hit - 1) {
-      const uint32_t e = __shfl_sync(0xffffffffu, own, __ffs(hit) - 1);
-      if (exc_owner(e) == lane) {
-        most++;
-        h.place2 = h.place;
-        h.e2 = h.e;
-        h.place = exc_place(e, key);
-        h.e = e;
-        h.select = exc_select(e);
-      }
+// takes the queue's next entry out
+__device__ __forceinline__ void exceptions_pull(Exceptions &x, uint32_t lane) {
+  x.set1 = x.set2;
+  x.entry1 = x.entry2;
+  x.set2 = kNever;
+  if (x.i < x.n) {
+    const uint32_t entry = x.q->entry[x.i][lane];
+    x.set2 = entry >> 2;
+    x.entry2 = entry | uint32_t(x.q->high[x.i][lane]) << 16;
+    x.i++;
+  }
+}
+__device__ __forceinline__ void exceptions_reset(Exceptions &x, uint32_t lane) {
+  __syncwarp();
+  x.q->count[lane] = 0;
+  x.n = x.i = 0;
+  x.set1 = x.set2 = kNever;
+  x.entry1 = x.entry2 = 0;
+  x.walk = false;
+  __syncwarp();
+}
+// all windows' entries are in the queues
+__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
+  __syncwarp();
+  x.n = x.q->count[lane];
+  x.walk = __any_sync(0xffffffffu, x.walk || x.n > kQueue);
+  if (x.walk) x.n = 0;
+  for (uint32_t i = 1; i < x.n; i++) {  // a few at most: by insertion
+    const uint16_t entry = x.q->entry[i][lane];
+    const uint8_t high = x.q->high[i][lane];
+    uint32_t j = i;
+    for (; j > 0 && x.q->entry[j - 1][lane] > entry; j--) {
+      x.q->entry[j][lane] = x.q->entry[j - 1][lane];
+      x.q->high[j][lane] = x.q->high[j - 1][lane];
     }
-  };
-  if (x.cnt > 0) hand(x.e, lane < x.cnt);
-  for (uint32_t i = 32; i < x.cnt; i += 32) hand(i + lane < x.cnt ? x.list[i + lane] : 0u, i + lane < x.cnt);
-  return __any_sync(0xffffffffu, most > 1) ? __any_sync(0xffffffffu, most > 2) ? 3 : 2 : 1;
+    x.q->entry[j][lane] = entry;
+    x.q->high[j][lane] = high;
+  }
+  exceptions_pull(x, lane);
+  exceptions_pull(x, lane);
+  __syncwarp();
+}
+// How many entries a lane has at most in the stage whose first subtile is
+// key: 1 (or none), 2, or 3 for more (or walk).
+__device__ __forceinline__ uint32_t exceptions_most(const Exceptions &x, uint32_t key, uint32_t lane) {
+  if (x.walk) return 3;
+  const bool two = x.set2 - 8 * key < 16;
+  if (!__any_sync(0xffffffffu, two)) return 1;
+  const bool three = two && x.i < x.n && (x.q->entry[x.i][lane] >> 2) - 8 * key < 16;
+  return __any_sync(0xffffffffu, three) ? 3 : 2;
+}
+// the stage is done
+__device__ __forceinline__ void exceptions_pass(Exceptions &x, uint32_t key, uint32_t lane) {
+  while (x.set1 - 8 * key < 16) exceptions_pull(x, lane);
 }
 // The container's exceptions among 4 values, the first at flat position f,
 // onto their high bytes.
@@ -470,17 +497,6 @@ static __device__ __noinline__ uint32_t exceptions_walk(uint32_t hi4, const uint
   }
   return hi4;
 }
-__device__ __forceinline__ void exceptions_reset(Exceptions &x) {
-  x.cnt = 0;
-  x.e = 0;
-  x.walk = false;
-  __syncwarp();  // the list may be written again
-}
-__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
-  __syncwarp();
-  x.e = lane < x.cnt ? x.list[lane] : 0u;
-}
-
 // A lane's 16 values of two rows of a subtile, as stored.
 struct Piece {
   uint2 idx[2];
@@ -524,7 +540,9 @@ struct StageAt {
 // which is slow one time in a hundred is felt).
 template <int kTiles, int kParts, bool kShare, bool kTwo>
 __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, uint4 book,
-                                              const Handed &h, uint32_t lane) {
+                                              const Exceptions &x, uint32_t lane) {
+  const uint32_t set1 = x.set1 - 8 * at.key, set2 = x.set2 - 8 * at.key, i1 = 4 * (x.entry1 & 3u);
+  const uint32_t sel1 = (0x3210u & ~(0xFu << i1)) | (6u << i1);
   Piece f[2];
   read_piece(f[0], at.slot, at.group, lane);
   read_piece(f[1], at.slot + kSubBytes, at.group, lane);
@@ -545,8 +563,8 @@ __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[
         const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
         const uint32_t lw = s == 0 ? f[sub].lo[r].x : s == 1 ? f[sub].lo[r].y : s == 2 ? f[sub].lo[r].z : f[sub].lo[r].w;
         uint32_t hi4 = high4(sel, up, book);
-        hi4 = h.place == uint32_t(8 * sub + 2 * s + r) ? prmt(hi4, h.e, h.select) : hi4;
-        if (kTwo) hi4 = h.place2 == uint32_t(8 * sub + 2 * s + r) ? prmt(hi4, h.e2, exc_select(h.e2)) : hi4;
+        if (set1 == uint32_t(8 * sub + 2 * s + r)) hi4 = prmt(hi4, x.entry1, sel1);
+        if (kTwo && set2 == uint32_t(8 * sub + 2 * s + r)) hi4 = put_high(hi4, x.entry2);
         const uint2 e = join4(lw, hi4);
         a[r] = e.x;
         a[r + 2] = e.y;
@@ -588,14 +606,12 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
         hi4 = exceptions_walk(hi4, v.exc_off, v.exc_pos, v.exc_val, v.ne,
                               at_row * K + kUnit * (sub ? at.unit1 : at.unit0) + 16 * t + 4 * s);
       } else {
-        for (uint32_t i = 0; i < x.cnt; i += 32) {
-          const uint32_t own = i + lane < x.cnt ? x.list[i + lane] : 0u;
-          uint32_t hit = __ballot_sync(0xffffffffu, i + lane < x.cnt && (exc_place(own, at.key) == 8 * sub + 2 * s + r));
-          for (; hit; hit &= hit - 1) {
-            const uint32_t e = __shfl_sync(0xffffffffu, own, __ffs(hit) - 1);
-            if (exc_owner(e) == lane) hi4 = prmt(hi4, e, exc_select(e));
-          }
-        }
+        const uint32_t set = 8 * (at.key + sub) + 2 * s + r;
+        if (x.set1 == set) hi4 = put_high(hi4, x.entry1);
+        if (x.set2 == set) hi4 = put_high(hi4, x.entry2);
+        for (uint32_t i = x.i; i < x.n && (x.q->entry[i][lane] >> 2) <= set; i++)
+          if ((x.q->entry[i][lane] >> 2) == set)
+            hi4 = put_high(hi4, x.q->entry[i][lane] | uint32_t(x.q->high[i][lane]) << 16);
       }
       const uint2 e = join4(lw, hi4);
       a[r] = e.x;

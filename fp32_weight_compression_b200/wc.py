@@ -713,10 +713,12 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
         plan_ptr, plan_bytes = plan.data_ptr(), plan.numel()
     y = _output(out, (M, N), torch.float32, dev)
     st = _status_word(status, dev)
-    work = torch.empty(M * r, dtype=torch.float32, device=dev)
-    _check((_lib or load()).wc12_linear_adapters(
+    lib = _lib or load()
+    work_bytes = lib.wc12_linear_adapters_work_bytes(M, r)
+    work = torch.empty(work_bytes, dtype=torch.uint8, device=dev)
+    _check(lib.wc12_linear_adapters(
         cont.data_ptr(), cont.numel(), plan_ptr or None, plan_bytes, N, K, x.data_ptr(), M, adapter.data_ptr(), a.data_ptr(),
-        b.data_ptr(), scales.data_ptr(), L, r, y.data_ptr(), work.data_ptr(), 4 * M * r, st.data_ptr(), _raw_stream(dev)),
+        b.data_ptr(), scales.data_ptr(), L, r, y.data_ptr(), work.data_ptr(), work_bytes, st.data_ptr(), _raw_stream(dev)),
         "wc12_linear_adapters")
     if status is None:
         check_status(st, "wc12_linear_adapters (device status)")
