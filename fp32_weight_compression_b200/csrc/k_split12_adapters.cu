@@ -262,14 +262,11 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
       const XAt xat = x_boxes(lane);
       Turn turn;
       for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
-        const uint32_t most = exceptions_most(x, u, lane);
+        const uint32_t most = exceptions_most(x, u);
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
         const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
         const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == u1, u, u, u + 1, row0, row0};
-        if (most == 1) stage_product<NT, 1, false, false>(tot0, tot1, at, xat, v.book, x, lane);
-        else if (most == 2) stage_product<NT, 1, false, true>(tot0, tot1, at, xat, v.book, x, lane);
-        else stage_product_slow<NT, 1, false>(tot0, tot1, at, xat, v, x, K, lane);
-        exceptions_pass(x, at.key, lane);
+        stage<NT, 1, false>(tot0, tot1, at, xat, v, x, most, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

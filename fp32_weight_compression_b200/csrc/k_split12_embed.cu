@@ -73,8 +73,9 @@ __global__ void __launch_bounds__(kMaxThreads) k12_embed(const __grid_constant__
   for (uint32_t c = 8 * tid; c < K; c += 8 * nthr) {
     const uint32_t q = *reinterpret_cast<const uint32_t *>(idx + c / 2);
     const uint2 l = *reinterpret_cast<const uint2 *>(lo + c);
-    const uint32_t sel = q & 0x77777777u, up = (q >> 3) & 0x11111111u;
-    const uint2 e0 = expand4(sel, up, v.book, l.x), e1 = expand4(sel >> 16, up >> 16, v.book, l.y);
+    uint32_t hi[2];
+    high8<false>(hi, q, v.book, 0);
+    const uint2 e0 = join4(l.x, hi[0]), e1 = join4(l.y, hi[1]);
     const uint32_t w[4] = {e0.x, e0.y, e1.x, e1.y};
     store8<kWide>(row, c, w, p.scale);
   }

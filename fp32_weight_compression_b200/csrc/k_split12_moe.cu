@@ -289,15 +289,12 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
     offsets(next, job + 2 * clusters);
     float gate[1][4] = {}, up[1][4] = {};
     for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
-      const uint32_t most = exceptions_most(x, 2 * u, lane);
+      const uint32_t most = exceptions_most(x, 2 * u);
       alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
       const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
-      if (most == 1) stage_product<1, 1, true, false>(gate, up, at, xat, v.book, x, lane);
-      else if (most == 2) stage_product<1, 1, true, true>(gate, up, at, xat, v.book, x, lane);
-      else stage_product_slow<1, 1, true>(gate, up, at, xat, v, x, K, lane);
-      exceptions_pass(x, at.key, lane);
+      stage<1, 1, true>(gate, up, at, xat, v, x, most, K, lane);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
@@ -446,15 +443,12 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       offsets(next, item + 2);
       float tot0[1][4] = {}, tot1[1][4] = {};
       for (; st < end; st++, q++, turn.next()) {
-        const uint32_t most = exceptions_most(x, 2 * st, lane);
+        const uint32_t most = exceptions_most(x, 2 * st);
         alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
         if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
         const StageAt at{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row_of(item), row_of(item)};
-        if (most == 1) stage_product<1, 2, false, false>(tot0, tot1, at, xat, v.book, x, lane);
-        else if (most == 2) stage_product<1, 2, false, true>(tot0, tot1, at, xat, v.book, x, lane);
-        else stage_product_slow<1, 2, false>(tot0, tot1, at, xat, v, x, K, lane);
-        exceptions_pass(x, at.key, lane);
+        stage<1, 2, false>(tot0, tot1, at, xat, v, x, most, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

@@ -108,7 +108,7 @@ __device__ __forceinline__ float cluster_load(const float *p, uint32_t rank) {
   uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), b;
   float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(b) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(b));
   return v;
 }
 
@@ -120,6 +120,10 @@ struct View {
   const uint8_t *exc_val;
   uint64_t n, ne;
   uint4 book;
+  // the codebook is base .. base + 7 and the same with the sign bit, as it is
+  // for weights spread alike to both sides of zero: base in each byte
+  bool runs;
+  uint32_t base4;
 };
 
 // The planes' places, and the start of the exceptions' lists, depend on the
@@ -148,6 +152,9 @@ __device__ __forceinline__ bool open_header(View &v, const uint8_t *w, uint64_t 
     return false;
   const wc12::Lay L = wc12::lay(n, v.ne);
   v.exc_val = w + L.off_excval;
+  v.base4 = (v.book.x & 0xFFu) * 0x01010101u;
+  v.runs = kk == 16 && (v.book.x & 0x80u) == 0 && (v.book.w >> 31) != 0 && v.book.x == v.base4 + 0x03020100u &&
+           v.book.y == v.base4 + 0x07060504u && v.book.z == (v.book.x | 0x80808080u) && v.book.w == (v.book.y | 0x80808080u);
   return q1.y == uint32_t(L.nc) && q2.x == L.off_idx && q2.y == L.off_lo && q3.x == L.off_exc && q3.y == L.total &&
          L.total <= w_bytes;
 }
@@ -306,27 +313,46 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   return d;
 }
 
-// wc12::expand4 with the selectors of 8 nibbles split beforehand: sel is the
-// entry within its half (3 bits), up 1 for entries 8..15, in the low 16 bits
-__device__ __forceinline__ uint32_t high4(uint32_t sel, uint32_t up, uint4 book) {
-  const uint32_t r0 = prmt(book.x, book.y, sel);
-  const uint32_t r1 = prmt(book.z, book.w, sel);
-  const uint32_t m = prmt(0x0000FF00u, 0u, up);
-  return (r0 & ~m) | (r1 & m);
+// The high bytes of 8 values, hi[0] the first 4's, from their 8 nibbles.  The
+// expansion is what bounds the products: byte permutes, shifts and logic
+// issue every other cycle, 64 a cycle and SM, against 29 values a cycle and SM
+// that come from memory.  By the codebook in registers (kRuns false) 8 values
+// take 13 of them and 4 to join the low bytes; where the codebook is two runs
+// the nibble's low bits and sign are put together instead: 7 and 4 (the
+// shift to the left and the sums go to the multiply-add pipe).
+template <bool kRuns>
+__device__ __forceinline__ void high8(uint32_t *hi, uint32_t q, uint4 book, uint32_t base4) {
+  if (kRuns) {
+    const uint32_t even = ((q & 0x07070707u) + base4) | ((q << 4) & 0x80808080u);
+    const uint32_t odd = (((q >> 4) & 0x07070707u) + base4) | (q & 0x80808080u);
+    hi[0] = prmt(even, odd, 0x5140);
+    hi[1] = prmt(even, odd, 0x7362);
+  } else {
+    const uint32_t sel = q & 0x77777777u, up = (q >> 3) & 0x11111111u;  // the entry within its half; which half
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const uint32_t si = sel >> (16 * i), m = prmt(0x0000FF00u, 0u, up >> (16 * i));
+      hi[i] = (prmt(book.x, book.y, si) & ~m) | (prmt(book.z, book.w, si) & m);
+    }
+  }
 }
 __device__ __forceinline__ uint2 join4(uint32_t lo4, uint32_t hi4) {
   return make_uint2(prmt(lo4, hi4, 0x5140), prmt(lo4, hi4, 0x7362));
 }
-__device__ __forceinline__ uint2 expand4(uint32_t sel, uint32_t up, uint4 book, uint32_t lo4) {
-  return join4(lo4, high4(sel, up, book));
-}
-
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same with nothing to add to
+__device__ __forceinline__ void mma_first(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // ---------------------------------------------------------------------------
 // Exceptions.  A lane's entry: which subtile, as the warp meets them (bits
 // 5-15), which of the lane's 8 sets of 4 values there (2 step + row half;
@@ -367,14 +393,16 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
   window_pairs(v, (e0 & ~uint64_t(1)) + 2 * lane, e1 <= v.ne ? e1 : 0, w.pos, w.val);
 }
 
-// A lane's exceptions: its queue of n entries, ascending, of which the next
-// two are out, as their set (entry >> 2) and the entry with its high byte in
-// bits 16-23.  walk (the same for the warp): too many, look them up.
+// A lane's exceptions, ascending: the next kOut of its queue are out, each as
+// its set (entry >> 2, kNever for none) and the entry with its high byte in
+// bits 16-23.  more: the n-entry queue of some lane of the warp has others, from
+// i on.  walk (the same for the warp): too many, look them up.
+constexpr int kOut = 4;
 struct Exceptions {
   Queues *q;
-  uint32_t n, i;  // entries, and the first that is not out
-  uint32_t set1, entry1, set2, entry2;
-  bool walk;
+  uint32_t n, i;
+  uint32_t set[kOut], entry[kOut];
+  bool more, walk;
 };
 // Entries have come: keeps those of the group's units [u0, u1), as of
 // subtile mul * unit + plus.
@@ -421,15 +449,14 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
     }
   }
 }
-// takes the queue's next entry out
-__device__ __forceinline__ void exceptions_pull(Exceptions &x, uint32_t lane) {
-  x.set1 = x.set2;
-  x.entry1 = x.entry2;
-  x.set2 = kNever;
+// the queue's next entry
+__device__ __forceinline__ void exceptions_pull(Exceptions &x, uint32_t &set, uint32_t &entry, uint32_t lane) {
+  set = kNever;
+  entry = 0;
   if (x.i < x.n) {
-    const uint32_t entry = x.q->entry[x.i][lane];
-    x.set2 = entry >> 2;
-    x.entry2 = entry | uint32_t(x.q->high[x.i][lane]) << 16;
+    const uint32_t e = x.q->entry[x.i][lane];
+    set = e >> 2;
+    entry = e | uint32_t(x.q->high[x.i][lane]) << 16;
     x.i++;
   }
 }
@@ -437,9 +464,12 @@ __device__ __forceinline__ void exceptions_reset(Exceptions &x, uint32_t lane) {
   __syncwarp();
   x.q->count[lane] = 0;
   x.n = x.i = 0;
-  x.set1 = x.set2 = kNever;
-  x.entry1 = x.entry2 = 0;
-  x.walk = false;
+#pragma unroll
+  for (int i = 0; i < kOut; i++) {
+    x.set[i] = kNever;
+    x.entry[i] = 0;
+  }
+  x.more = x.walk = false;
   __syncwarp();
 }
 // all windows' entries are in the queues
@@ -448,10 +478,12 @@ __device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
   x.n = x.q->count[lane];
   x.walk = __any_sync(0xffffffffu, x.walk || x.n > kQueue);
   if (x.walk) x.n = 0;
+#pragma unroll 1
   for (uint32_t i = 1; i < x.n; i++) {  // a few at most: by insertion
     const uint16_t entry = x.q->entry[i][lane];
     const uint8_t high = x.q->high[i][lane];
     uint32_t j = i;
+#pragma unroll 1
     for (; j > 0 && x.q->entry[j - 1][lane] > entry; j--) {
       x.q->entry[j][lane] = x.q->entry[j - 1][lane];
       x.q->high[j][lane] = x.q->high[j - 1][lane];
@@ -459,22 +491,31 @@ __device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
     x.q->entry[j][lane] = entry;
     x.q->high[j][lane] = high;
   }
-  exceptions_pull(x, lane);
-  exceptions_pull(x, lane);
-  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kOut; i++) exceptions_pull(x, x.set[i], x.entry[i], lane);
+  x.more = __any_sync(0xffffffffu, x.i < x.n);
 }
 // How many entries a lane has at most in the stage whose first subtile is
-// key: 1 (or none), 2, or 3 for more (or walk).
-__device__ __forceinline__ uint32_t exceptions_most(const Exceptions &x, uint32_t key, uint32_t lane) {
+// key: 0, 1, 2, or 3 for more (or walk).
+__device__ __forceinline__ uint32_t exceptions_most(const Exceptions &x, uint32_t key) {
   if (x.walk) return 3;
-  const bool two = x.set2 - 8 * key < 16;
-  if (!__any_sync(0xffffffffu, two)) return 1;
-  const bool three = two && x.i < x.n && (x.q->entry[x.i][lane] >> 2) - 8 * key < 16;
-  return __any_sync(0xffffffffu, three) ? 3 : 2;
+  if (!__any_sync(0xffffffffu, x.set[0] - 8 * key < 16)) return 0;
+  if (!__any_sync(0xffffffffu, x.set[1] - 8 * key < 16)) return 1;
+  return __any_sync(0xffffffffu, x.set[2] - 8 * key < 16) ? 3 : 2;
 }
-// the stage is done
-__device__ __forceinline__ void exceptions_pass(Exceptions &x, uint32_t key, uint32_t lane) {
-  while (x.set1 - 8 * key < 16) exceptions_pull(x, lane);
+// the stage is done: its entries go, the next ones move up
+__device__ __forceinline__ void exceptions_pass(Exceptions &x, uint32_t key, uint32_t most, uint32_t lane) {
+  for (uint32_t j = 0; j < most; j++) {
+    const bool gone = x.set[0] - 8 * key < 16;
+#pragma unroll
+    for (int i = 0; i + 1 < kOut; i++) {
+      x.set[i] = gone ? x.set[i + 1] : x.set[i];
+      x.entry[i] = gone ? x.entry[i + 1] : x.entry[i];
+    }
+    if (gone) x.set[kOut - 1] = kNever;
+    if (x.more && x.set[kOut - 1] == kNever) exceptions_pull(x, x.set[kOut - 1], x.entry[kOut - 1], lane);
+    if (most == 3 && __any_sync(0xffffffffu, x.set[0] - 8 * key < 16)) j = 0;
+  }
 }
 // The container's exceptions among 4 values, the first at flat position f,
 // onto their high bytes.
@@ -535,47 +576,50 @@ struct StageAt {
 // added up in the tensor cores, subtiles in fp32 registers: the tensor cores
 // cut off what their accumulator cannot hold, so that long sums there drift
 // toward zero.  Columns without a token hold sums that the caller drops.
-// kTwo: a lane may have two exceptions (one stage in a hundred, where the
-// containers have one in 2,500 values; four warps share a stage, so that code
-// which is slow one time in a hundred is felt).
-template <int kTiles, int kParts, bool kShare, bool kTwo>
-__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, uint4 book,
+// kMost: exceptions that a lane may have (two in one stage in a hundred, where
+// the containers have one in 2,500 values; four warps share a stage, so that
+// code which is slow one time in a hundred is felt).
+template <int kTiles, int kParts, bool kShare, bool kRuns, int kMost>
+__device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, const View &v,
                                               const Exceptions &x, uint32_t lane) {
-  const uint32_t set1 = x.set1 - 8 * at.key, set2 = x.set2 - 8 * at.key, i1 = 4 * (x.entry1 & 3u);
+  const uint32_t set1 = x.set[0] - 8 * at.key, set2 = x.set[1] - 8 * at.key, i1 = 4 * (x.entry[0] & 3u);
   const uint32_t sel1 = (0x3210u & ~(0xFu << i1)) | (6u << i1);
   Piece f[2];
   read_piece(f[0], at.slot, at.group, lane);
   read_piece(f[1], at.slot + kSubBytes, at.group, lane);
-  float d[2][kTiles][4] = {};
+  float d[2][kTiles][4];
   uint4 xv[2][kTiles][kParts];
 #pragma unroll
-  for (int s = 0; s < 4; s++) {
-    if ((s & 1) == 0) {  // 8 values of each token, for two steps
-      read_values<kTiles, kParts>(xv[0], at.xs + (s ? xat.second : xat.first), at.tile_bytes);
-      if (!kShare) read_values<kTiles, kParts>(xv[1], at.xs2 + (s ? xat.second : xat.first), at.tile_bytes);
-    }
+  for (int w = 0; w < 2; w++) {  // 8 values of a row: two steps
+    read_values<kTiles, kParts>(xv[0], at.xs + (w ? xat.second : xat.first), at.tile_bytes);
+    if (!kShare) read_values<kTiles, kParts>(xv[1], at.xs2 + (w ? xat.second : xat.first), at.tile_bytes);
 #pragma unroll
     for (int sub = 0; sub < 2; sub++) {
-      uint32_t a[4];
+      uint32_t a[2][4];
 #pragma unroll
       for (int r = 0; r < 2; r++) {
-        const uint32_t qw = s < 2 ? f[sub].idx[r].x : f[sub].idx[r].y;
-        const uint32_t sel = (qw & 0x77777777u) >> (16 * (s & 1)), up = ((qw >> 3) & 0x11111111u) >> (16 * (s & 1));
-        const uint32_t lw = s == 0 ? f[sub].lo[r].x : s == 1 ? f[sub].lo[r].y : s == 2 ? f[sub].lo[r].z : f[sub].lo[r].w;
-        uint32_t hi4 = high4(sel, up, book);
-        if (set1 == uint32_t(8 * sub + 2 * s + r)) hi4 = prmt(hi4, x.entry1, sel1);
-        if (kTwo && set2 == uint32_t(8 * sub + 2 * s + r)) hi4 = put_high(hi4, x.entry2);
-        const uint2 e = join4(lw, hi4);
-        a[r] = e.x;
-        a[r + 2] = e.y;
+        uint32_t hi[2];
+        high8<kRuns>(hi, w ? f[sub].idx[r].y : f[sub].idx[r].x, v.book, v.base4);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const uint32_t set = 8 * sub + 2 * (2 * w + i) + r;
+          if (kMost > 0 && set1 == set) hi[i] = prmt(hi[i], x.entry[0], sel1);
+          if (kMost > 1 && set2 == set) hi[i] = put_high(hi[i], x.entry[1]);
+          const uint2 e = join4(w ? i ? f[sub].lo[r].w : f[sub].lo[r].z : i ? f[sub].lo[r].y : f[sub].lo[r].x, hi[i]);
+          a[i][r] = e.x;
+          a[i][r + 2] = e.y;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kTiles; i++)
+      for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int part = 0; part < kParts; part++) {
-          const uint4 q = xv[kShare ? 0 : sub][i][part];
-          mma(d[sub][i], a, s & 1 ? q.z : q.x, s & 1 ? q.w : q.y);
-        }
+        for (int tile = 0; tile < kTiles; tile++)
+#pragma unroll
+          for (int part = 0; part < kParts; part++) {
+            const uint4 q = xv[kShare ? 0 : sub][tile][part];
+            if (w == 0 && i == 0 && part == 0) mma_first(d[sub][tile], a[i], q.x, q.y);
+            else mma(d[sub][tile], a[i], i ? q.z : q.x, i ? q.w : q.y);
+          }
     }
   }
 #pragma unroll
@@ -600,15 +644,18 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
     for (uint32_t r = 0; r < 2; r++) {
       const uint32_t row = at.group * kRows + g + 8 * r;
       const uint32_t q = shared2(from + row * 32 + 8 * t + 2 * s), lw = shared4(from + kIdxBytes + row * 64 + 16 * t + 4 * s);
-      uint32_t hi4 = high4(q & 0x7777u, (q >> 3) & 0x1111u, v.book);
+      uint32_t hi[2];
+      high8<false>(hi, q, v.book, 0);
+      uint32_t hi4 = hi[0];
       if (x.walk) {
         const uint64_t at_row = (sub ? at.row1 : at.row0) + g + 8 * r;
         hi4 = exceptions_walk(hi4, v.exc_off, v.exc_pos, v.exc_val, v.ne,
                               at_row * K + kUnit * (sub ? at.unit1 : at.unit0) + 16 * t + 4 * s);
       } else {
         const uint32_t set = 8 * (at.key + sub) + 2 * s + r;
-        if (x.set1 == set) hi4 = put_high(hi4, x.entry1);
-        if (x.set2 == set) hi4 = put_high(hi4, x.entry2);
+#pragma unroll
+        for (int i = 0; i < kOut; i++)
+          if (x.set[i] == set) hi4 = put_high(hi4, x.entry[i]);
         for (uint32_t i = x.i; i < x.n && (x.q->entry[i][lane] >> 2) <= set; i++)
           if ((x.q->entry[i][lane] >> 2) == set)
             hi4 = put_high(hi4, x.q->entry[i][lane] | uint32_t(x.q->high[i][lane]) << 16);
@@ -633,6 +680,23 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
       }
     }
   }
+}
+
+// The one of these that the stage needs.
+template <int kTiles, int kParts, bool kShare>
+__device__ __forceinline__ void stage(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, const View &v,
+                                      Exceptions &x, uint32_t most, uint32_t K, uint32_t lane) {
+  if (most == 3) {
+    stage_product_slow<kTiles, kParts, kShare>(tot0, tot1, at, xat, v, x, K, lane);
+  } else if (v.runs) {
+    if (most == 0) stage_product<kTiles, kParts, kShare, true, 0>(tot0, tot1, at, xat, v, x, lane);
+    else if (most == 1) stage_product<kTiles, kParts, kShare, true, 1>(tot0, tot1, at, xat, v, x, lane);
+    else stage_product<kTiles, kParts, kShare, true, 2>(tot0, tot1, at, xat, v, x, lane);
+  } else {
+    if (most < 2) stage_product<kTiles, kParts, kShare, false, 1>(tot0, tot1, at, xat, v, x, lane);
+    else stage_product<kTiles, kParts, kShare, false, 2>(tot0, tot1, at, xat, v, x, lane);
+  }
+  if (most > 0) exceptions_pass(x, at.key, most, lane);
 }
 
 // A warp's sums of a group, [token][row] with kRedTok floats a token.
