@@ -43,8 +43,6 @@ struct Params {
   const uint16_t *a, *b;   // [L, r, K], [L, N, r]
   const float *scale;      // [L]
   float *t;                // [M, r], or three planes of bf16
-  uint32_t *tickets;       // few tokens: [kMaxTickets], zeroed by the first kernel
-  float *parts;            // and two segments' sums of each CTA
   float *y;                // [M, N]
   uint32_t M, N, K, r, L;
   int32_t *status;
@@ -170,8 +168,6 @@ __global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_
   __shared__ float red[kSideWarps][kTokens * kRedTok];
   __shared__ float part[kTokens * 16];
   const uint32_t lane = threadIdx.x & 31;
-  if (kTiles == 1 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    for (uint32_t i = threadIdx.x; i < kMaxTickets; i += kSideThreads) p.tickets[i] = 0;
   const uint32_t rank = blockIdx.x % csize, m0 = kTokens * (blockIdx.x / csize), j0 = 16 * blockIdx.y, z = blockIdx.z;
   int32_t ad = -1;
   if (lane < kTokens && m0 + lane < p.M) ad = p.adapter[m0 + lane];
@@ -190,232 +186,179 @@ __global__ void __launch_bounds__(kSideThreads) k12_adapter_shrink(const __grid_
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: blocks of 64 weight rows, all tokens.  A stage's two subtiles
-// are successive ranges of K.
+// Few tokens: a CTA takes 64 weight rows and all tokens, the CTAs of a
+// cluster split K.  A stage's two subtiles are successive ranges of K.
 template <int NT>
 struct Few {
   static constexpr uint32_t kXBox = NT * 1024;  // 8 NT tokens' values of a unit
   static constexpr uint32_t kStage = 2 * kSubBytes + 2 * kXBox;
+  static constexpr uint32_t kOwn = own_words(8 * NT);  // words of a warp: its list, then its sums
   static constexpr uint32_t kQueues = kDepth * kStage;
-  static constexpr uint32_t kBars = kQueues + kWarps * uint32_t(sizeof(Queues));
+  static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = 1024 + kBars + sizeof(Bars);  // 1024: the boxes' swizzle counts from there
-  static constexpr uint32_t kPart = 4 * NT * kConsumers;          // floats of a segment's sums, 4 NT a lane
 };
 
-// A lane's sums of block b (rows g and g + 8 of its warp's 16, tokens 8 i + 2 t
-// and the one after) with their adapters' part into Y.
 template <int NT>
-__device__ __forceinline__ void put_rows(const Params &p, uint32_t row0, const float tot[NT][4], uint32_t lane) {
-  const uint32_t g = lane >> 2, t = lane & 3;
-  int32_t ad[NT][2];
-  const uint4 *pb[NT][2];
-  const float4 *pt[NT][2];
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < NT; i++)
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-      const uint32_t m = 8 * i + 2 * t + c;
-      ad[i][c] = m < p.M ? p.adapter[m] : -1;
-      if (ad[i][c] >= int32_t(p.L)) ad[i][c] = -1;
-      any = any || ad[i][c] >= 0;
-      // a token without one reads some other's, and drops it: the loads need
-      // no condition
-      pb[i][c] = reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad[i][c] >= 0 ? ad[i][c] : 0) * p.N + row0 + g) * p.r);
-      pt[i][c] = reinterpret_cast<const float4 *>(p.t + uint64_t(m < p.M ? m : 0u) * p.r);
-    }
-  float add[NT][4] = {};
-  if (__any_sync(0xffffffffu, any)) {
-#pragma unroll 1
-    for (uint32_t j = 0; j < p.r / 8; j++) {
-      uint4 b[NT][2][2];
-      float4 q[NT][2][2];
-#pragma unroll
-      for (int i = 0; i < NT; i++)
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-          b[i][c][0] = pb[i][c][j];
-          b[i][c][1] = pb[i][c][p.r + j];  // 8 rows on
-          q[i][c][0] = pt[i][c][2 * j];
-          q[i][c][1] = pt[i][c][2 * j + 1];
-        }
-#pragma unroll
-      for (int i = 0; i < NT; i++)
-#pragma unroll
-        for (int c = 0; c < 2; c++)
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint4 w = b[i][c][h];
-            const float4 t0 = q[i][c][0], t1 = q[i][c][1];
-            add[i][2 * h + c] += t0.x * bf16_lo(w.x) + t0.y * bf16_hi(w.x) + t0.z * bf16_lo(w.y) + t0.w * bf16_hi(w.y) +
-                                 t1.x * bf16_lo(w.z) + t1.y * bf16_hi(w.z) + t1.z * bf16_lo(w.w) + t1.w * bf16_hi(w.w);
-          }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NT; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const uint32_t m = 8 * i + 2 * t + (j & 1);
-      if (m < p.M) p.y[uint64_t(m) * p.N + row0 + g + 8 * (j >> 1)] = ad[i][j & 1] >= 0 ? tot[i][j] + add[i][j] : tot[i][j];
-    }
-}
-
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 3) k12_few_adapters(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_constant__ Params p,
                                                                 const __grid_constant__ Planes planes,
-                                                                const __grid_constant__ CUtensorMap tm_x) {
+                                                                const __grid_constant__ CUtensorMap tm_x, uint32_t csize) {
   using F = Few<NT>;
   extern __shared__ __align__(128) uint8_t raw[];
-  uint8_t *dyn = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+  uint8_t *dyn = raw + (1024 - smem_u32(raw) % 1024) % 1024;  // the same place in every CTA of the cluster
   Bars &bars = *reinterpret_cast<Bars *>(dyn + F::kBars);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t K = p.K, units = K / kUnit, per = (units + 1) / 2;
-  const Deal deal(p.N / kSubRows, per);
-  const uint64_t q0 = deal.begin(blockIdx.x), q1 = deal.begin(blockIdx.x + 1);
-  const uint32_t first = uint32_t(q0 / per), last = uint32_t((q1 - 1) / per), s_first = uint32_t(q0 - uint64_t(first) * per);
+  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kSubRows;
+  const uint32_t K = p.K, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
   const uint32_t ring = smem_u32(dyn);
   View v;
   open_planes(v, p.w, uint64_t(p.N) * K);
   if (tid == 0) bars_init(bars);
   __syncthreads();
+  bool ok;
+  float *red = reinterpret_cast<float *>(dyn + F::kQueues);
   if (warp == kWarps) {
     Turn turn;
-    uint32_t block = first, s = s_first;
-    auto load = [&] {
+    auto load = [&](uint32_t u) {
       if (lane == 0) {
         uint64_t *full = &bars.full[turn.slot];
-        const uint32_t slot = ring + turn.slot * F::kStage, u = 2 * s, subs = u + 1 < units ? 2 : 1;
+        const uint32_t slot = ring + turn.slot * F::kStage, subs = u + 1 < u1 ? 2 : 1;
         bar_expect(full, subs * (kSubBytes + F::kXBox));
         for (uint32_t i = 0; i < subs; i++) {
-          load_subtile(slot + i * kSubBytes, planes, (u + i) * kUnit, block * kSubRows, full);
+          load_subtile(slot + i * kSubBytes, planes, (u + i) * kUnit, n0, full);
           load_box(slot + 2 * kSubBytes + i * F::kXBox, &tm_x, (u + i) * kUnit, 0, full);
         }
       }
       __syncwarp();
-      if (++s == per) {
-        s = 0;
-        block++;
-      }
-      turn.next();
     };
-    uint32_t n = 0;
-    const uint32_t all = uint32_t(q1 - q0);
-    for (; n < kDepth && n < all; n++) load();
-    const bool ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
+    uint32_t u = u0;
+    for (uint32_t i = 0; i < kDepth && u < u1; i++, u += 2, turn.next()) load(u);
+    ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
     // B's rows for the tokens' adapters, on their way to L2 for the end
     if (lane < p.M) {
       const int32_t ad = p.adapter[lane];
-      if (ad >= 0 && ad < int32_t(p.L))
-        prefetch_l2(p.b + (uint64_t(ad) * p.N + first * kSubRows) * p.r, (last - first + 1) * kSubRows * p.r * 2);
+      if (ad >= 0 && ad < int32_t(p.L)) prefetch_l2(p.b + (uint64_t(ad) * p.N + n0) * p.r, kSubRows * p.r * 2);
     }
-    for (; ok && n < all; n++) {
+    for (; ok && u < u1; u += 2, turn.next()) {
       if (!bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) break;
-      load();
+      load(u);
     }
-    finish_copies(bars, turn, n, p.status);  // no copy is in flight when the CTA ends
-    return;
-  }
-  auto row_of = [&](uint32_t block) { return block * kSubRows + kRows * warp; };
-  // the exceptions of a block are in flight during the one before, their
-  // offsets during the one before that
-  Window now, next;
-  window_offsets(now, v.exc_off, row_of(first), K, lane);
-  if (first < last) window_offsets(next, v.exc_off, row_of(first + 1), K, lane);
-  if (!open_header(v, p.w, p.w_bytes)) {
-    if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
-    wait_prerequisites();
-    return;
-  }
-  if (v.ne > 0) window_entries(now, v, lane);
-  Exceptions x;
-  x.q = reinterpret_cast<Queues *>(dyn + F::kQueues + warp * sizeof(Queues));
-  const XAt xat = x_boxes(lane);
-  Turn turn;
-  bool alive = true;
-  uint64_t q = q0;
-  for (uint32_t block = first, s = s_first; q < q1; block++, s = 0) {
-    const uint32_t s0 = s, end = q1 - q < per - s ? s + uint32_t(q1 - q) : per, row0 = row_of(block);
+    // no copy is in flight when the CTA ends
+    finish_copies(bars, turn, (u - u0) / 2, p.status);
+  } else {
+    const uint32_t row0 = n0 + kRows * warp;
+    Window win;
+    window_offsets(win, v.exc_off, row0, K, lane);
+    Exceptions x;
+    x.q = reinterpret_cast<Queues *>(dyn + F::kQueues + warp * F::kOwn * 4);
     exceptions_reset(x, lane);
-    if (v.ne > 0) {
-      window_keep(x, now, v, row0, K, 2 * s, 2 * end, 1, 0, lane, p.status);
-      exceptions_ready(x, lane);
-      now = next;
-      if (block < last) window_entries(now, v, lane);
-      if (block + 1 < last) window_offsets(next, v.exc_off, row_of(block + 2), K, lane);
-    }
-    float tot[NT][4] = {}, tot1[NT][4] = {};
-    for (; s < end; s++, q++, turn.next()) {
-      const uint32_t u = 2 * s, most = exceptions_most(x, u);
-      alive = alive && bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
-      if (!alive) {  // on to the end, with the others' barriers
-        q += end - s;
-        break;
+    ok = open_header(v, p.w, p.w_bytes);
+    float tot0[NT][4] = {}, tot1[NT][4] = {};
+    if (ok) {
+      if (v.ne > 0) {
+        window_entries(win, v, lane);
+        window_keep(x, win, v, row0, K, u0, u1, 1, 0, lane, p.status);
+        exceptions_ready(x, lane);
       }
-      const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
-      const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == units, u, u, u + 1, row0, row0};
-      stage<NT, 1, false>(tot, tot1, at, xat, v, x, most, K, lane);
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
+      const XAt xat = x_boxes(lane);
+      Turn turn;
+      for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
+        const uint32_t most = exceptions_most(x, u);
+        if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
+        const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
+        const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == u1, u, u, u + 1, row0, row0};
+        stage<NT, 1, false>(tot0, tot1, at, xat, v, x, most, K, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
+      }
+    } else if (blockIdx.x == 0 && tid == 0) {
+      report(p.status, WC_ERR_CORRUPT);
     }
 #pragma unroll
     for (int i = 0; i < NT; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) tot[i][j] += tot1[i][j];
-    wait_prerequisites();  // t, and the tickets
-    if (s0 > 0 || end < per) {
-      const uint32_t c0 = deal.cta_of(uint64_t(block) * per), c1 = deal.cta_of(uint64_t(block + 1) * per - 1);
-      // a CTA's first segment's sums, then its last one's
-      auto part_of = [&](uint32_t cta) {
-        const uint32_t which = uint32_t(deal.begin(cta) / per) == block ? 0u : 1u;
-        return reinterpret_cast<float4 *>(p.parts + (2 * uint64_t(cta) + which) * F::kPart) + tid;
-      };
-#pragma unroll
-      for (int i = 0; i < NT; i++)
-        __stcg(part_of(blockIdx.x) + i * kConsumers, make_float4(tot[i][0], tot[i][1], tot[i][2], tot[i][3]));
-      if (!last_ticket(p.tickets, c0, c1 - c0 + 1, &bars.last)) continue;
-#pragma unroll
-      for (int i = 0; i < NT; i++) tot[i][0] = tot[i][1] = tot[i][2] = tot[i][3] = 0.0f;
-#pragma unroll 4
-      for (uint32_t c = c0; c <= c1; c++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) {
-          const float4 f = __ldcg(part_of(c) + i * kConsumers);
-          tot[i][0] += f.x;
-          tot[i][1] += f.y;
-          tot[i][2] += f.z;
-          tot[i][3] += f.w;
-        }
-    }
-    put_rows<NT>(p, row0, tot, lane);
+      for (int j = 0; j < 4; j++) tot0[i][j] += tot1[i][j];
+    __syncwarp();
+    put_sums<NT>(red + warp * F::kOwn, tot0, lane);
   }
+  // a thread has one row of every so many tokens; their adapters, and the
+  // first 16 ranks' values of B, are read before the others are waited for
+  constexpr uint32_t kOut = 8 * NT * kSubRows / kConsumers;
+  const uint32_t row = tid % kSubRows, m0 = tid / kSubRows + kConsumers / kSubRows * rank, per = kConsumers / kSubRows * csize;
+  int32_t ad[kOut];
+  uint4 b0[kOut], b1[kOut];
+  const bool puts = ok && warp < kWarps;
+#pragma unroll
+  for (uint32_t i = 0; i < kOut; i++) {
+    const uint32_t m = m0 + i * per;
+    ad[i] = puts && m < p.M ? p.adapter[m] : -1;
+    if (ad[i] >= int32_t(p.L)) ad[i] = -1;
+  }
+  auto b_of = [&](uint32_t i) { return reinterpret_cast<const uint4 *>(p.b + (uint64_t(ad[i]) * p.N + n0 + row) * p.r); };
+#pragma unroll
+  for (uint32_t i = 0; i < kOut; i++) {
+    b0[i] = b1[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (ad[i] >= 0) {
+      b0[i] = b_of(i)[0];
+      if (p.r > 8) b1[i] = b_of(i)[1];
+    }
+  }
+  if (csize > 1) cluster_sync(); else __syncthreads();
+  wait_prerequisites();  // t
+  if (puts) {
+#pragma unroll
+    for (uint32_t i = 0; i < kOut; i++) {
+      const uint32_t m = m0 + i * per;
+      if (m >= p.M) break;
+      const float *from = red + row / kRows * F::kOwn + m * kRedTok + row % kRows;
+      float sum = 0.0f;
+      for (uint32_t c = 0; c < csize; c++) sum += csize > 1 ? cluster_load(from, c) : *from;
+      if (ad[i] >= 0) {
+        const float4 *pt = reinterpret_cast<const float4 *>(p.t + uint64_t(m) * p.r);
+        float add = 0.0f;
+        auto take = [&](uint4 b, uint32_t j) {
+          const float4 t0 = pt[2 * j], t1 = pt[2 * j + 1];
+          add += t0.x * bf16_lo(b.x) + t0.y * bf16_hi(b.x) + t0.z * bf16_lo(b.y) + t0.w * bf16_hi(b.y);
+          add += t1.x * bf16_lo(b.z) + t1.y * bf16_hi(b.z) + t1.z * bf16_lo(b.w) + t1.w * bf16_hi(b.w);
+        };
+        take(b0[i], 0);
+        if (p.r > 8) take(b1[i], 1);
+        for (uint32_t j = 2; j < p.r / 8; j++) take(b_of(i)[j], j);
+        sum += add;
+      }
+      p.y[uint64_t(m) * p.N + n0 + row] = sum;
+    }
+  }
+  if (csize > 1) cluster_sync();  // the others' sums are read until here
 }
 
-// the CTAs of the few-token kernel on the device (three an SM), the kernels
-// set up
-int few_ctas() {
+// the device's SMs, the kernels set up
+int device_sms() {
   static DeviceSetup setup;
   return setup.get([] {
-    if (cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) != cudaSuccess ||
-        cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) != cudaSuccess)
-      return 0;
-    const int ctas = 3 * wc12l::device_sms();
-    return ctas < int(kMaxTickets) ? ctas : int(kMaxTickets);
+    return cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) == cudaSuccess &&
+                   cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) ==
+                       cudaSuccess
+               ? wc12l::device_sms() : 0;
   });
 }
 
 template <int NT>
-int32_t launch_few(const Params &p, uint32_t ctas, cudaStream_t s) {
+int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   using F = Few<NT>;
-  const uint64_t stages = uint64_t(p.N / kSubRows) * ((p.K / kUnit + 1) / 2);
   Planes planes;
   CUtensorMap tm_x;
   if (!make_planes(planes, p.w, p.N, p.K) ||
       !wc12l::make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, p.K, p.M, uint64_t(p.K) * 2, kUnit, 8 * NT,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
     return WC_ERR_CUDA;
-  return launch(k12_few_adapters<NT>, dim3(ctas < stages ? ctas : uint32_t(stages)), kThreads, 1, F::kSmem, s, true, p, planes, tm_x) == cudaSuccess ? WC_OK
-                                                                                                               : WC_ERR_CUDA;
+  // CTAs that split K: as many as run at once (4 an SM), while each fills
+  // its ring
+  const uint32_t blocks = p.N / kSubRows, units = p.K / kUnit;
+  uint32_t csize = 1;
+  while (csize < 8 && blocks * csize * 2 <= 4u * uint32_t(sms) && units >= 4 * csize * kDepth) csize *= 2;
+  return launch(k12_few_adapters<NT>, dim3(blocks * csize), kThreads, csize, F::kSmem, s, true, p, planes, tm_x, csize) ==
+                 cudaSuccess
+             ? WC_OK : WC_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -485,22 +428,9 @@ __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __gr
 
 }  // namespace wc12a
 
-namespace {
-// The workspace: t; with few tokens then the tickets and the segments' sums.
-struct Work {
-  uint64_t tickets, parts, total;
-};
-Work work_of(uint32_t M, uint32_t r) {
-  using namespace wc12a;
-  Work w;
-  w.tickets = (uint64_t(M) * r * (M <= kFewTokens ? 4 : 6) + 127) / 128 * 128;
-  w.parts = w.tickets + kMaxTickets * 4;
-  w.total = M > kFewTokens ? w.tickets : w.parts + 2ull * kMaxTickets * 4 * (M <= 8 ? Few<1>::kPart : Few<2>::kPart);
-  return w;
+extern "C" uint64_t wc12_linear_adapters_work_bytes(uint32_t M, uint32_t r) {
+  return uint64_t(M) * r * (M <= wc12a::kFewTokens ? 4 : 6);
 }
-}  // namespace
-
-extern "C" uint64_t wc12_linear_adapters_work_bytes(uint32_t M, uint32_t r) { return work_of(M, r).total; }
 
 extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes,
                                         uint32_t N, uint32_t K, const void *d_x, uint32_t M, const int32_t *d_adapter,
@@ -518,7 +448,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   if (L == 0 || L > 0x7FFFFFFFu || r == 0 || r % 8 != 0 || r > kMaxRank || K > kMaxK || N / (kRows * kSideWarps) > 65535 || M > 0x7FFFFFFFu)
     return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_linear_adapters_work_bytes(M, r)) return WC_ERR_CAPACITY;
-  const int ctas = few_ctas(), sms = ctas > 0 ? wc12l::device_sms() : 0;
+  const int sms = device_sms();
   if (sms <= 0) return WC_ERR_CUDA;
   Params p;
   p.w = static_cast<const uint8_t *>(d_w);
@@ -529,8 +459,6 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
   p.b = static_cast<const uint16_t *>(d_b);
   p.scale = d_scale;
   p.t = static_cast<float *>(d_work);
-  p.tickets = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(d_work) + work_of(M, r).tickets);
-  p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(d_work) + work_of(M, r).parts);
   p.y = d_y;
   p.M = M;
   p.N = N;
@@ -550,7 +478,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
                false, p, csize) != cudaSuccess)
       return WC_ERR_CUDA;
   }
-  if (M <= kFewTokens) return M <= 8 ? launch_few<1>(p, uint32_t(ctas), s) : launch_few<2>(p, uint32_t(ctas), s);
+  if (M <= kFewTokens) return M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s);
   if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kSideWarps)), kSideThreads, 1, 0, s, true, p) != cudaSuccess)
     return WC_ERR_CUDA;
   return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, true, d_status, stream);

@@ -52,8 +52,6 @@ struct Params {
   const uint16_t *x;    // [T, H]
   const float *logits;  // [T, E]
   Route *route;
-  uint32_t *tickets;    // [kMaxTickets] of the up product, then of the down product; zeroed with the route
-  float *parts;         // two segments' sums of each CTA, of one product, then of the other
   uint16_t *hs;         // two planes of [T k, F]
   void *out;            // [T, H]
   uint32_t T, E, H, F, k;
@@ -86,7 +84,6 @@ __global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_co
     key[i] = e < p.E ? order_key(p.logits[uint64_t(m) * p.E + e]) : 0u;
   }
   for (uint32_t e = tid; e < p.E; e += blockDim.x) who[e] = 0;
-  for (uint32_t i = tid; i < 2 * kMaxTickets; i += blockDim.x) p.tickets[i] = 0;
   __syncthreads();
   uint32_t mine = 0, mine_e = 0, top = 0;  // lane j: the j-th largest key and its expert
   {
@@ -184,11 +181,11 @@ constexpr uint32_t align128(uint32_t v) { return (v + 127) / 128 * 128; }
 
 struct Up {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 8 * kXRow);
+  static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its list, then its sums of G_e and U_e
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
-  static constexpr uint32_t kBars = kQueues + kWarps * uint32_t(sizeof(Queues));
+  static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = kBars + sizeof(Bars);
-  static constexpr uint32_t kPart = 8 * kConsumers;  // floats of a segment's sums, 8 a lane
 };
 
 // p_e silu(gate) up as two bf16 numbers, each rounded to nearest: off by at
@@ -200,13 +197,14 @@ __device__ __forceinline__ void put_gated(uint16_t *dst, uint64_t plane, float g
   dst[plane] = uint16_t((hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(h - __uint_as_float(hi << 16)));
 }
 
-// A block (a job) is 64 rows of G_e and the same of U_e for one item, a
-// stage's two subtiles those rows with the same values of H.
-__global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant__ Params p, const __grid_constant__ Planes planes) {
+// A stage's two subtiles: 64 rows of G_e and of U_e, the same values of H.
+__global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant__ Params p,
+                                                          const __grid_constant__ Planes planes, uint32_t csize) {
   extern __shared__ __align__(128) uint8_t dyn[];
   Route &r = *reinterpret_cast<Route *>(dyn + Up::kRoute);
   Bars &bars = *reinterpret_cast<Bars *>(dyn + Up::kBars);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % csize, first = blockIdx.x / csize, clusters = gridDim.x / csize;
   View v;
   open_planes(v, p.gate_up, uint64_t(p.E) * 2 * p.F * p.H);
   const bool ok = open_header(v, p.gate_up, p.gate_up_bytes);  // the same for every thread
@@ -219,37 +217,38 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant_
     if (blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
     return;
   }
-  const uint32_t K = p.H, per = K / kUnit, tiles = p.F / kSubRows, ring = smem_u32(dyn);
-  const Deal deal(r.items * tiles, per);
-  if (blockIdx.x >= deal.ctas) return;
-  const uint64_t q0 = deal.begin(blockIdx.x), q1 = deal.begin(blockIdx.x + 1);
-  const uint32_t first = uint32_t(q0 / per), last = uint32_t((q1 - 1) / per), u_first = uint32_t(q0 - uint64_t(first) * per);
+  const uint32_t K = p.H, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
+  const uint32_t tiles = p.F / kSubRows, jobs = r.items * tiles, ring = smem_u32(dyn);
   Turn turn;
   if (warp == kWarps) {
-    uint32_t n = 0;
+    uint32_t s = 0;
     bool alive = true;
-    for (uint32_t job = first, u = u_first; alive && job <= last; job++, u = 0) {
-      const uint32_t item = job / tiles, columns = r.item_n[item];
+    for (uint32_t job = first; alive && job < jobs; job += clusters) {
+      const uint32_t item = job / tiles, n = r.item_n[item];
       const uint32_t row = uint32_t(r.item_e[item]) * 2 * p.F + (job - item * tiles) * kSubRows;
       const uint16_t *px = p.x;
-      if (lane < columns) px += uint64_t(r.pair[r.item_first[item] + lane] / p.k) * K;
-      for (; u < per && n < uint32_t(q1 - q0); u++, n++, turn.next()) {
-        if (n >= kDepth && !bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) {
+      if (lane < n) px += uint64_t(r.pair[r.item_first[item] + lane] / p.k) * K;
+      for (uint32_t u = u0; u < u1; u++, s++, turn.next()) {
+        if (s >= kDepth && !bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) {
           alive = false;
           break;
         }
         uint64_t *full = &bars.full[turn.slot];
         const uint32_t slot = ring + turn.slot * Up::kStage;
         if (lane == 0) {
-          bar_expect(full, 2 * kSubBytes + columns * 2 * kUnit);
+          bar_expect(full, 2 * kSubBytes + n * 2 * kUnit);
           load_subtile(slot, planes, u * kUnit, row, full);
           load_subtile(slot + kSubBytes, planes, u * kUnit, row + p.F, full);
         }
         __syncwarp();
-        if (lane < columns) load_row(slot + 2 * kSubBytes + lane * kXRow, px + u * kUnit, 2 * kUnit, full);
+        if (lane < n) load_row(slot + 2 * kSubBytes + lane * kXRow, px + u * kUnit, 2 * kUnit, full);
       }
     }
-    finish_copies(bars, turn, n, p.status);  // no copy is in flight when the CTA ends
+    finish_copies(bars, turn, s, p.status);
+    if (csize > 1 && first < jobs) {  // with the others' barriers
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
   auto row_of = [&](uint32_t job, uint32_t which) {
@@ -260,152 +259,125 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_up(const __grid_constant_
   // offsets during the one before that
   Window now[2], next[2];
   auto offsets = [&](Window *w, uint32_t job) {
-    if (v.ne > 0 && job <= last)
+    if (v.ne > 0 && job < jobs)
       for (uint32_t i = 0; i < 2; i++) window_offsets(w[i], v.exc_off, row_of(job, i), K, lane);
   };
   auto entries = [&](Window *w, uint32_t job) {
-    if (v.ne > 0 && job <= last)
+    if (v.ne > 0 && job < jobs)
       for (uint32_t i = 0; i < 2; i++) window_entries(w[i], v, lane);
   };
   offsets(now, first);
-  offsets(next, first + 1);
+  offsets(next, first + clusters);
   entries(now, first);
   Exceptions x;
-  x.q = reinterpret_cast<Queues *>(dyn + Up::kQueues + warp * sizeof(Queues));
+  x.q = reinterpret_cast<Queues *>(dyn + Up::kQueues + warp * Up::kOwn * 4);
+  float *sums = reinterpret_cast<float *>(dyn + Up::kQueues);
   const uint64_t plane = uint64_t(p.T) * p.k * p.F;
   const XAt xat = x_rows(lane);
   const uint32_t g = lane >> 2, t = lane & 3;
   bool alive = true;
-  uint64_t q = q0;
-  for (uint32_t job = first, u = u_first; q < q1; job++, u = 0) {
-    const uint32_t begin = u, end = q1 - q < per - u ? u + uint32_t(q1 - q) : per;
+  for (uint32_t job = first; job < jobs; job += clusters) {
     exceptions_reset(x, lane);
     if (v.ne > 0) {
 #pragma unroll 1
-      for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u, end, 2, i, lane, p.status);
+      for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
       exceptions_ready(x, lane);
     }
     now[0] = next[0];
     now[1] = next[1];
-    entries(now, job + 1);
-    offsets(next, job + 2);
-    const uint64_t row0 = row_of(job, 0), row1 = row_of(job, 1);
+    entries(now, job + clusters);
+    offsets(next, job + 2 * clusters);
     float gate[1][4] = {}, up[1][4] = {};
-    for (; u < end; u++, q++, turn.next()) {
+    for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
       const uint32_t most = exceptions_most(x, 2 * u);
-      alive = alive && bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
-      if (!alive) {  // on to the end, with the others' barriers
-        q += end - u;
-        break;
-      }
+      alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
+      if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
-      const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row0, row1};
+      const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
       stage<1, 1, true>(gate, up, at, xat, v, x, most, K, lane);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
-    if (begin > 0 || end < per) {
-      const uint32_t c0 = deal.cta_of(uint64_t(job) * per), c1 = deal.cta_of(uint64_t(job + 1) * per - 1);
-      // a CTA's first segment's sums, then its last one's
-      auto part_of = [&](uint32_t cta) {
-        const uint32_t which = uint32_t(deal.begin(cta) / per) == job ? 0u : 1u;
-        return reinterpret_cast<float4 *>(p.parts + (2 * uint64_t(cta) + which) * Up::kPart) + tid;
-      };
-      __stcg(part_of(blockIdx.x), make_float4(gate[0][0], gate[0][1], gate[0][2], gate[0][3]));
-      __stcg(part_of(blockIdx.x) + kConsumers, make_float4(up[0][0], up[0][1], up[0][2], up[0][3]));
-      if (!last_ticket(p.tickets, c0, c1 - c0 + 1, &bars.last)) continue;
-#pragma unroll
-      for (int i = 0; i < 4; i++) gate[0][i] = up[0][i] = 0.0f;
-#pragma unroll 4
-      for (uint32_t c = c0; c <= c1; c++) {
-        const float4 a = __ldcg(part_of(c)), b = __ldcg(part_of(c) + kConsumers);
-        gate[0][0] += a.x;
-        gate[0][1] += a.y;
-        gate[0][2] += a.z;
-        gate[0][3] += a.w;
-        up[0][0] += b.x;
-        up[0][1] += b.y;
-        up[0][2] += b.z;
-        up[0][3] += b.w;
-      }
-    }
     const uint32_t item = job / tiles, n = r.item_n[item], from = r.item_first[item], f0 = (job - item * tiles) * kSubRows;
+    if (csize == 1) {  // a lane has both sums of its rows and columns
 #pragma unroll
-    for (uint32_t i = 0; i < 4; i++) {  // a lane has both sums of its rows and columns
-      const uint32_t c = 2 * t + (i & 1), row = f0 + kRows * warp + g + 8 * (i >> 1);
-      if (c < n)
-        put_gated(p.hs + uint64_t(r.pair[from + c]) * p.F + row, plane, gate[0][i], up[0][i], r.weight[from + c]);
+      for (uint32_t i = 0; i < 4; i++) {
+        const uint32_t c = 2 * t + (i & 1), row = f0 + kRows * warp + g + 8 * (i >> 1);
+        if (c < n) {
+          const uint32_t pair = r.pair[from + c];
+          put_gated(p.hs + uint64_t(pair) * p.F + row, plane, gate[0][i], up[0][i], r.weight[from + c]);
+        }
+      }
+      continue;
     }
+    __syncwarp();
+    put_sums<1>(sums + warp * Up::kOwn, gate, lane);
+    put_sums<1>(sums + warp * Up::kOwn + 8 * kRedTok, up, lane);
+    cluster_sync();
+    for (uint32_t o = tid + rank * kConsumers; o < n * kSubRows; o += kConsumers * csize) {
+      const uint32_t row = o % kSubRows, c = o / kSubRows;
+      const float *at = sums + row / kRows * Up::kOwn + c * kRedTok + row % kRows;
+      float a = 0.0f, b = 0.0f;
+      for (uint32_t i = 0; i < csize; i++) {
+        a += cluster_load(at, i);
+        b += cluster_load(at + 8 * kRedTok, i);
+      }
+      const uint32_t pair = r.pair[from + c];
+      put_gated(p.hs + uint64_t(pair) * p.F + f0 + row, plane, a, b, r.weight[from + c]);
+    }
+    cluster_sync();  // the others' sums are read until here
   }
 }
 
 // ---------------------------------------------------------------------------
-// A block is 64 rows of the output, its stages those of D_e's rows for every
-// item, one item after another; a stage's two subtiles are successive ranges
-// of F.
+// A stage's two subtiles are successive ranges of F.
 struct Down {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 16 * kXRow);
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
   static constexpr uint32_t kBars = kQueues + kWarps * uint32_t(sizeof(Queues));
   static constexpr uint32_t kAcc = align128(kBars + uint32_t(sizeof(Bars)));
-  static constexpr uint32_t kPart = kSubRows;  // floats of a segment's sums and token
   static __host__ __device__ uint32_t smem(uint32_t T) { return kAcc + kWarps * T * kRedTok * 4; }
 };
 
-__global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constant__ Params p, const __grid_constant__ Planes planes) {
+__global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constant__ Params p,
+                                                            const __grid_constant__ Planes planes, uint32_t csize) {
   extern __shared__ __align__(128) uint8_t dyn[];
   Route &r = *reinterpret_cast<Route *>(dyn + Down::kRoute);
   Bars &bars = *reinterpret_cast<Bars *>(dyn + Down::kBars);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % csize, n0 = blockIdx.x / csize * kSubRows;
   View v;
   open_planes(v, p.down, uint64_t(p.E) * p.H * p.F);
   const bool ok = open_header(v, p.down, p.down_bytes);  // the same for every thread
   if (tid == 0) bars_init(bars);
+  float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
+  if (warp < kWarps)
+    for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
   take_route(r, p.route, p.T * p.k);  // the up product's CTAs had it before this one could start
   __syncthreads();
-  const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2;  // stages of an item
-  const uint32_t all = r.items * per, blocks = p.H / kSubRows, ring = smem_u32(dyn);
-  if (all == 0) {  // no token has an expert
-    wait_prerequisites();
-    for (uint64_t i = uint64_t(blockIdx.x) * kThreads + tid; i < uint64_t(p.T) * p.H; i += uint64_t(gridDim.x) * kThreads) {
-      if (p.wide) static_cast<float *>(p.out)[i] = 0.0f;
-      else static_cast<uint16_t *>(p.out)[i] = 0;
-    }
-    return;
-  }
-  const Deal deal(blocks, all);
-  if (!ok || blockIdx.x >= deal.ctas) {
-    if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
-    wait_prerequisites();
-    return;
-  }
-  const uint64_t q0 = deal.begin(blockIdx.x), q1 = deal.begin(blockIdx.x + 1);
-  // where a stage of the deal is: the block, the item, the item's stage
-  struct At {
-    uint32_t block, item, st;
-  };
-  auto at_of = [&](uint64_t q) {
-    const uint32_t block = uint32_t(q / all), in = uint32_t(q - uint64_t(block) * all);
-    return At{block, in / per, in - in / per * per};
-  };
-  auto step = [&](At &a) {
-    if (++a.st == per) {
-      a.st = 0;
-      if (++a.item == r.items) {
-        a.item = 0;
-        a.block++;
-      }
-    }
-  };
+  // the items' stages one after another; this CTA's: [q0, q1)
+  const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2, all = r.items * per, ring = smem_u32(dyn);
+  const uint32_t q0 = ok ? uint32_t(uint64_t(all) * rank / csize) : 0u, q1 = ok ? uint32_t(uint64_t(all) * (rank + 1) / csize) : 0u;
+  const uint32_t first = q0 / per, st0 = q0 - first * per;  // item, stage of it
+  if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
   Turn turn;
   if (warp == kWarps) {
     const uint64_t plane = uint64_t(p.T) * p.k * p.F;
+    struct At {
+      uint32_t item, st;
+    } at{first, st0};
+    auto step = [&](At &a) {
+      if (++a.st == per) {
+        a.st = 0;
+        a.item++;
+      }
+    };
     auto subs_of = [&](uint32_t st) { return 2 * st + 1 < units ? 2u : 1u; };
     auto weights = [&](const Turn &turn, const At &a) {
       uint64_t *full = &bars.full[turn.slot];
       const uint32_t slot = ring + turn.slot * Down::kStage, subs = subs_of(a.st);
-      const uint32_t row = uint32_t(r.item_e[a.item]) * p.H + a.block * kSubRows;
+      const uint32_t row = uint32_t(r.item_e[a.item]) * p.H + n0;
       if (lane == 0) {
         bar_expect(full, subs * (kSubBytes + r.item_n[a.item] * 4 * kUnit));
         for (uint32_t i = 0; i < subs; i++) load_subtile(slot + i * kSubBytes, planes, (2 * a.st + i) * kUnit, row, full);
@@ -421,87 +393,68 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
     };
     // the weights of the first stages are on their way before hs is waited
     // for, its values follow
-    uint32_t n = 0;
-    At at = at_of(q0);
-    for (; q0 + n < q1 && n < kDepth; n++, turn.next()) {
+    uint32_t s = 0;
+    for (; q0 + s < q1 && s < kDepth; s++, turn.next()) {
       weights(turn, at);
       step(at);
     }
     wait_prerequisites();
     asm volatile("fence.proxy.async.global;" ::: "memory");
     Turn turn2;
-    At at2 = at_of(q0);
-    for (uint32_t i = 0; i < n; i++, turn2.next()) {
+    At at2{first, st0};
+    for (uint32_t i = 0; i < s; i++, turn2.next()) {
       values(turn2, at2);
       step(at2);
     }
-    for (; q0 + n < q1; n++, turn.next()) {
+    for (; q0 + s < q1; s++, turn.next()) {
       if (!bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) break;
       weights(turn, at);
       values(turn, at);
       step(at);
     }
-    finish_copies(bars, turn, n, p.status);
-    return;
-  }
-  float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
-  const uint32_t g = lane >> 2, t = lane & 3;
-  auto row_of = [&](const At &a) { return uint64_t(r.item_e[a.item]) * p.H + a.block * kSubRows + kRows * warp; };
-  // the windows go from item to item, and on to the next block's first
-  const At end_at = at_of(q1 - 1);
-  auto after = [&](At a) {
-    a.st = per - 1;
-    step(a);
-    return a;
-  };
-  auto has = [&](const At &a) { return v.ne > 0 && (a.block < end_at.block || (a.block == end_at.block && a.item <= end_at.item)); };
-  At at = at_of(q0);
-  Window now, next;
-  if (has(at)) window_offsets(now, v.exc_off, row_of(at), K, lane);
-  if (has(after(at))) window_offsets(next, v.exc_off, row_of(after(at)), K, lane);
-  if (has(at)) window_entries(now, v, lane);
-  Exceptions x;
-  x.q = reinterpret_cast<Queues *>(dyn + Down::kQueues + warp * sizeof(Queues));
-  const XAt xat = x_rows(lane);
-  bool alive = true;
-  uint64_t q = q0;
-  while (q < q1) {
-    const uint32_t block = at.block, begin = uint32_t(q - uint64_t(block) * all);
-    const uint64_t block_end = q1 < uint64_t(block + 1) * all ? q1 : uint64_t(block + 1) * all;
-    for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
-    __syncwarp();
-    while (q < block_end) {  // an item
-      const uint32_t item = at.item;
-      const uint64_t left = block_end - q;
-      uint32_t st = at.st;
-      const uint32_t end = left < per - st ? st + uint32_t(left) : per;
-      const uint64_t row0 = row_of(at);
+    finish_copies(bars, turn, s, p.status);
+  } else if (q0 < q1) {
+    const uint32_t row0 = n0 + kRows * warp, last = (q1 - 1) / per;
+    auto row_of = [&](uint32_t item) { return uint64_t(r.item_e[item]) * p.H + row0; };
+    Window now, next;
+    auto offsets = [&](Window &w, uint32_t i) {
+      if (v.ne > 0 && i <= last) window_offsets(w, v.exc_off, row_of(i), K, lane);
+    };
+    auto entries = [&](Window &w, uint32_t i) {
+      if (v.ne > 0 && i <= last) window_entries(w, v, lane);
+    };
+    offsets(now, first);
+    offsets(next, first + 1);
+    entries(now, first);
+    Exceptions x;
+    x.q = reinterpret_cast<Queues *>(dyn + Down::kQueues + warp * sizeof(Queues));
+    const XAt xat = x_rows(lane);
+    uint32_t st = st0;
+    bool alive = true;
+    for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
+      const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
       exceptions_reset(x, lane);
       if (v.ne > 0) {
-        window_keep(x, now, v, row0, K, 2 * st, 2 * end, 1, 0, lane, p.status);
+        window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
         exceptions_ready(x, lane);
       }
       now = next;
-      const At at1 = after(at), at2 = after(at1);
-      if (has(at1)) window_entries(now, v, lane);
-      if (has(at2)) window_offsets(next, v.exc_off, row_of(at2), K, lane);
+      entries(now, item + 1);
+      offsets(next, item + 2);
       float tot0[1][4] = {}, tot1[1][4] = {};
       for (; st < end; st++, q++, turn.next()) {
         const uint32_t most = exceptions_most(x, 2 * st);
-        alive = alive && bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
-        if (!alive) {  // on to the end, with the others' barriers
-          q += end - st;
-          break;
-        }
+        alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
+        if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
-        const StageAt sa{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row0, row0};
-        stage<1, 2, false>(tot0, tot1, sa, xat, v, x, most, K, lane);
+        const StageAt at{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row_of(item), row_of(item)};
+        stage<1, 2, false>(tot0, tot1, at, xat, v, x, most, K, lane);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }
       // columns to tokens; a token that did not choose the expert gets
       // nothing (not even zero times an infinite weight)
-      const uint32_t n = r.item_n[item], from = r.item_first[item];
+      const uint32_t n = r.item_n[item], from = r.item_first[item], g = lane >> 2, t = lane & 3;
 #pragma unroll
       for (uint32_t i = 0; i < 2; i++)
         if (2 * t + i < n) {
@@ -509,67 +462,46 @@ __global__ void __launch_bounds__(kThreads, 2) k12_moe_down(const __grid_constan
           to[0] += tot0[0][i] + tot1[0][i];
           to[8] += tot0[0][2 + i] + tot1[0][2 + i];
         }
-      at = at1;
     }
-    __syncwarp();
-    const bool whole = begin == 0 && block_end == uint64_t(block + 1) * all;
-    const uint32_t c0 = deal.cta_of(uint64_t(block) * all), c1 = deal.cta_of(uint64_t(block + 1) * all - 1);
-    // a CTA's first segment's sums, then its last one's, a warp's [token][row]
-    auto part_of = [&](uint32_t cta) {
-      const uint32_t which = uint32_t(deal.begin(cta) / all) == block ? 0u : 1u;
-      return p.parts + (2 * uint64_t(cta) + which) * Down::kPart * p.T + warp * kRows * p.T;
-    };
-    if (!whole) {
-      float *mine = part_of(blockIdx.x);
-      for (uint32_t i = lane; i < p.T * kRows; i += 32) __stcg(mine + i, acc[i / kRows * kRedTok + i % kRows]);
-      wait_prerequisites();  // the tickets are zero since before this kernel could start
-      if (!last_ticket(p.tickets + kMaxTickets, c0, c1 - c0 + 1, &bars.last)) continue;
-    }
-    for (uint32_t i = lane; i < p.T * kRows; i += 32) {
-      float sum = 0.0f;
-      if (whole) {
-        sum = acc[i / kRows * kRedTok + i % kRows];
-      } else {
-#pragma unroll 4
-        for (uint32_t c = c0; c <= c1; c++) sum += __ldcg(part_of(c) + i);
-      }
-      const uint64_t to = uint64_t(i / kRows) * p.H + block * kSubRows + kRows * warp + i % kRows;
-      if (p.wide) static_cast<float *>(p.out)[to] = sum;
-      else static_cast<uint16_t *>(p.out)[to] = uint16_t(bf16_bits(sum));
-    }
-    __syncwarp();  // acc is read until here
   }
+  if (csize > 1) cluster_sync(); else __syncthreads();
+  wait_prerequisites();
+  if (ok) {
+    const float *sums = reinterpret_cast<const float *>(dyn + Down::kAcc);
+    for (uint32_t o = tid + rank * kThreads; o < p.T * kSubRows; o += kThreads * csize) {
+      const uint32_t row = o % kSubRows, m = o / kSubRows;
+      const float *from = sums + (row / kRows * p.T + m) * kRedTok + row % kRows;
+      float sum = 0.0f;
+      for (uint32_t c = 0; c < csize; c++) sum += csize > 1 ? cluster_load(from, c) : *from;
+      const uint64_t at = uint64_t(m) * p.H + n0 + row;
+      if (p.wide) static_cast<float *>(p.out)[at] = sum;
+      else static_cast<uint16_t *>(p.out)[at] = uint16_t(bf16_bits(sum));
+    }
+  }
+  if (csize > 1) cluster_sync();  // the others' sums are read until here
 }
 
-// the device's SMs, the kernels set up
-int moe_sms() {
+// the CTAs of the up product that run at once on the device, the kernels set
+// up
+int up_slots() {
   static DeviceSetup setup;
   return setup.get([] {
-    return cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) == cudaSuccess &&
-                   cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) ==
-                       cudaSuccess
-               ? wc12l::device_sms() : 0;
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
+        cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess)
+      return 0;
+    return per_sm * wc12l::device_sms();
   });
-}
-
-// The workspace of a slice of at most kMaxTokens tokens.
-struct Work {
-  uint64_t tickets, parts, hs, total;
-};
-Work work_of(uint32_t T, uint32_t k, uint32_t F) {
-  const uint64_t t = T < kMaxTokens ? T : kMaxTokens;
-  Work w;
-  w.tickets = align128(sizeof(Route));
-  w.parts = w.tickets + 2 * kMaxTickets * 4;
-  const uint64_t up = Up::kPart, down = Down::kPart * t;  // the down product's come after the up product's are read
-  w.hs = w.parts + 2ull * kMaxTickets * 4 * (up > down ? up : down);
-  w.total = w.hs + t * k * F * 4;
-  return w;
 }
 
 }  // namespace wc12m
 
-extern "C" uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F) { return wc12m::work_of(T, k, F).total; }
+extern "C" uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F) {
+  const uint64_t t = T < wc12m::kMaxTokens ? T : wc12m::kMaxTokens;
+  return wc12m::align128(sizeof(wc12m::Route)) + t * k * F * 4;
+}
 
 extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const void *d_down, uint64_t down_bytes,
                             uint32_t E, uint32_t H, uint32_t F, const void *d_x, const float *d_logits, uint32_t T,
@@ -590,19 +522,15 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   if (d_x == nullptr || d_logits == nullptr || d_out == nullptr || d_work == nullptr) return WC_ERR_INVALID_ARG;
   if (!aligned(d_x, 16) || !aligned(d_logits, 4) || !aligned(d_out, 4) || !aligned(d_work, 16)) return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_moe_work_bytes(T, k, F)) return WC_ERR_CAPACITY;
-  const int sms = moe_sms();
+  const int slots = up_slots(), sms = slots > 0 ? wc12l::device_sms() : 0;
   if (sms <= 0) return WC_ERR_CUDA;
   Params p;
   p.gate_up = static_cast<const uint8_t *>(d_gate_up);
   p.gate_up_bytes = gate_up_bytes;
   p.down = static_cast<const uint8_t *>(d_down);
   p.down_bytes = down_bytes;
-  const Work w = work_of(T, k, F);
-  uint8_t *work = static_cast<uint8_t *>(d_work);
-  p.route = reinterpret_cast<Route *>(work);
-  p.tickets = reinterpret_cast<uint32_t *>(work + w.tickets);
-  p.parts = reinterpret_cast<float *>(work + w.parts);
-  p.hs = reinterpret_cast<uint16_t *>(work + w.hs);
+  p.route = static_cast<Route *>(d_work);
+  p.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(d_work) + align128(sizeof(Route)));
   p.E = E;
   p.H = H;
   p.F = F;
@@ -618,15 +546,21 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     p.x = static_cast<const uint16_t *>(d_x) + uint64_t(m) * H;
     p.logits = d_logits + uint64_t(m) * E;
     p.out = static_cast<uint8_t *>(d_out) + uint64_t(m) * H * (p.wide ? 4 : 2);
-    // CTAs that run at once: three an SM of the up product, two of the down
-    // product (what its stages leave room for)
-    const uint32_t most_up = 3u * uint32_t(sms) < kMaxTickets ? 3u * uint32_t(sms) : kMaxTickets;
-    const uint32_t most_down = 2u * uint32_t(sms) < kMaxTickets ? 2u * uint32_t(sms) : kMaxTickets;
+    // up: clusters that split H until about 4 CTAs an SM have work; with
+    // more jobs than that, as many CTAs as run at once
+    const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows);
+    uint32_t cu = 1;
+    while (cu < 8 && jobs * cu * 2 <= 4u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
+    // down: CTAs that split the items, the same
+    const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
+    uint32_t cd = 1;
+    while (cd < 16 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
-        launch(k12_moe_up, dim3(most_up), kThreads, 1, Up::kSmem, s, true, p, up) != cudaSuccess ||
-        launch(k12_moe_down, dim3(most_down), kThreads, 1, Down::smem(p.T), s, true, p, down) != cudaSuccess)
+        launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, Up::kSmem, s, true, p, up, cu) !=
+            cudaSuccess ||
+        launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;
   }
   return WC_OK;

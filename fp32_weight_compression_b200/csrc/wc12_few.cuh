@@ -73,7 +73,7 @@ constexpr uint32_t kUnit = 64;       // values of K of a subtile
 constexpr uint32_t kMaxK = 1 << 16;  // a group's rows touch at most 17 chunks
 constexpr uint32_t kQueue = 16;      // exceptions a lane keeps
 constexpr uint32_t kRedTok = 18;     // floats a token's 16 sums take (padded: few bank conflicts)
-constexpr uint32_t kDepth = 4;       // stages of the ring
+constexpr uint32_t kDepth = 3;       // stages of the ring
 constexpr uint32_t kSpinLimit = 1u << 24;
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
@@ -194,12 +194,16 @@ __device__ __forceinline__ uint2 shared8(uint32_t a) {
   return v;
 }
 
-// A warp's lanes' queues of exceptions.
+// A warp's own part of shared memory: its lanes' queues, then its sums.
 struct Queues {
   uint32_t count[32];
   uint16_t entry[kQueue][32];
   uint8_t high[kQueue][32];
 };
+constexpr uint32_t own_words(uint32_t tokens) {
+  return tokens * kRedTok * 4 > sizeof(Queues) ? tokens * kRedTok : uint32_t(sizeof(Queues)) / 4;
+}
+
 __device__ __forceinline__ uint32_t shared4(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -211,43 +215,9 @@ __device__ __forceinline__ uint32_t shared2(uint32_t a) {
   return v;
 }
 
-// Work is dealt out as stages: `blocks` blocks of rows with `per` stages each
-// are one long row, of which every CTA takes an equal part, whatever the
-// sizes: no CTA waits for another, and all end together.  A CTA's part of a
-// block is a segment; where a block's segments are of several CTAs, each
-// leaves its sums in the workspace and takes a ticket, and the one with the
-// last ticket adds them up in the CTAs' order.  (Clusters that split K came
-// first: they started 4 to 10 us late where the kernel before still had an SM
-// of theirs, and ended 14 us apart.)
-struct Deal {
-  uint32_t per, ctas;  // ctas: those that have work, a stage each at least
-  uint64_t total;
-  __device__ __forceinline__ Deal(uint32_t blocks, uint32_t per_) : per(per_), total(uint64_t(blocks) * per_) {
-    ctas = total < gridDim.x ? uint32_t(total) : gridDim.x;
-  }
-  __device__ __forceinline__ uint64_t begin(uint32_t cta) const { return total * cta / ctas; }
-  __device__ __forceinline__ uint32_t cta_of(uint64_t stage) const { return uint32_t(((stage + 1) * ctas - 1) / total); }
-};
-constexpr uint32_t kMaxTickets = 1024;  // CTAs of a launch, at most
-// all multiplying warps
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
-// Takes a ticket of the block whose first segment is of CTA `first`, after
-// this CTA's sums were written by its multiplying warps (which all call it);
-// true for the last of `count` segments, whose CTA may read all of them then.
-__device__ __forceinline__ bool last_ticket(uint32_t *tickets, uint32_t first, uint32_t count, uint32_t *flag) {
-  __threadfence();
-  consumers_sync();
-  if (threadIdx.x == 0) *flag = atomicAdd(&tickets[first], 1u) + 1 == count;
-  consumers_sync();
-  const bool last = *static_cast<volatile uint32_t *>(flag) != 0;
-  if (last) __threadfence();
-  return last;
-}
-
 struct Bars {
   uint64_t full[kDepth], empty[kDepth];
   int failed;
-  uint32_t last;  // last_ticket's
 };
 // by one thread, before a barrier of the CTA
 __device__ __forceinline__ void bars_init(Bars &b) {
