@@ -34,6 +34,7 @@ constexpr uint32_t kFewTokens = 16;
 constexpr uint32_t kMaxRank = 256;
 // of the two small products with A and B
 constexpr int kSideWarps = 4, kSideThreads = 32 * kSideWarps;
+constexpr uint32_t kDepth = 3;  // stages of the ring, for four CTAs an SM
 
 struct Params {
   const uint8_t *w;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
   bool ok;
   float *red = reinterpret_cast<float *>(dyn + F::kQueues);
   if (warp == kWarps) {
-    Turn turn;
+    Turn<kDepth> turn;
     auto load = [&](uint32_t u) {
       if (lane == 0) {
         uint64_t *full = &bars.full[turn.slot];
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
         exceptions_ready(x, lane);
       }
       const XAt xat = x_boxes(lane);
-      Turn turn;
+      Turn<kDepth> turn;
       for (uint32_t u = u0; u < u1; u += 2, turn.next()) {
         const uint32_t most = exceptions_most(x, u);
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
@@ -336,6 +337,7 @@ int device_sms() {
   static DeviceSetup setup;
   return setup.get([] {
     return cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) == cudaSuccess &&
+                   share_sm(k12_adapter_shrink<1>) &&
                    cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) ==
                        cudaSuccess
                ? wc12l::device_sms() : 0;

@@ -2,11 +2,14 @@
 // container (wc12_embed, include/wc_split12.h): out[t] = scale * table[ids[t]],
 // the rows asked for read at 12 bits a value, the rest of the table never.
 //
-// A CTA expands one row: a thread takes 8 values at a time (4 index bytes, 8
-// low bytes, 16 or 32 bytes out).  The row's exceptions are a short run in
-// the list of each 65,536-value chunk that it touches (usually one); the CTA
-// looks through the list, or first narrows it down when it is long, and
-// writes the exceptions' values over the row after a barrier.
+// A CTA expands one row: a thread takes pieces of 8 values (4 index bytes, 8
+// low bytes, 16 or 32 bytes out), four of them at once, so that a row is on
+// its way as a whole.  The row's exceptions are a short run in the list of
+// each 65,536-value chunk that it touches (usually one): their offsets are
+// read beside the row's bytes, the list's entries before the row is written,
+// and the exceptions' values go over it after a barrier.  A long list is
+// narrowed down first.  Latency bounds few rows (id, row, write: three round
+// trips), the memory's rate many.
 #include <cstdint>
 
 #include "wc12_few.cuh"
@@ -16,6 +19,7 @@ namespace wc12e {
 using namespace wc12f;
 
 constexpr uint32_t kMaxThreads = 256;
+constexpr uint32_t kBatch = 4;  // pieces of 8 values of a thread at once
 
 struct Params {
   const uint8_t *w;
@@ -69,20 +73,46 @@ __global__ void __launch_bounds__(kMaxThreads) k12_embed(const __grid_constant__
   }
   const uint64_t f0 = uint64_t(id) * K, f1 = f0 + K;
   const uint8_t *idx = v.idx + f0 / 2, *lo = v.lo + f0;
-#pragma unroll 2
-  for (uint32_t c = 8 * tid; c < K; c += 8 * nthr) {
-    const uint32_t q = *reinterpret_cast<const uint32_t *>(idx + c / 2);
-    const uint2 l = *reinterpret_cast<const uint2 *>(lo + c);
-    uint32_t hi[2];
-    high8<false>(hi, q, v.book, 0);
-    const uint2 e0 = join4(l.x, hi[0]), e1 = join4(l.y, hi[1]);
-    const uint32_t w[4] = {e0.x, e0.y, e1.x, e1.y};
-    store8<kWide>(row, c, w, p.scale);
+  // the first chunk's list: its offsets now, this thread's entry once they
+  // have come
+  uint64_t ch = f0 / kChunk, e0 = v.exc_off[ch], e1 = v.exc_off[ch + 1];
+  uint32_t pos = 0, high = 0;
+  auto entry = [&] {
+    if (v.ne > 0 && e0 + tid < e1 && e1 <= v.ne) {
+      pos = v.exc_pos[e0 + tid];
+      high = v.exc_val[e0 + tid];
+    }
+  };
+  if (8 * tid >= K) entry();  // no piece of the row
+  for (uint32_t c0 = 8 * tid; c0 < K; c0 += 8 * kBatch * nthr) {
+    uint32_t q[kBatch];
+    uint2 l[kBatch];
+#pragma unroll
+    for (uint32_t i = 0; i < kBatch; i++) {
+      const uint32_t c = c0 + 8 * i * nthr < K ? c0 + 8 * i * nthr : c0;
+      q[i] = *reinterpret_cast<const uint32_t *>(idx + c / 2);
+      l[i] = *reinterpret_cast<const uint2 *>(lo + c);
+    }
+    if (c0 == 8 * tid) entry();
+#pragma unroll
+    for (uint32_t i = 0; i < kBatch; i++) {
+      const uint32_t c = c0 + 8 * i * nthr;
+      if (c >= K) break;
+      uint32_t hi[2];
+      high8<false>(hi, q[i], v.book, 0);
+      const uint2 a = join4(l[i].x, hi[0]), b = join4(l[i].y, hi[1]);
+      const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+      store8<kWide>(row, c, w, p.scale);
+    }
   }
   if (v.ne == 0) return;
   __syncthreads();
-  for (uint64_t ch = f0 / kChunk; ch * kChunk < f1; ch++) {
-    uint64_t e0 = v.exc_off[ch], e1 = v.exc_off[ch + 1];
+  const uint64_t ch0 = ch;
+  for (; ch * kChunk < f1; ch++) {
+    if (ch > ch0) {
+      e0 = e1;
+      e1 = v.exc_off[ch + 1];
+    }
     if (e0 > e1 || e1 > v.ne) {
       if (tid == 0) report(p.status, WC_ERR_CORRUPT);
       continue;
@@ -91,26 +121,28 @@ __global__ void __launch_bounds__(kMaxThreads) k12_embed(const __grid_constant__
     const uint32_t b = f0 > ch * kChunk ? uint32_t(f0 - ch * kChunk) : 0u;
     const uint64_t left = f1 - ch * kChunk;
     const uint32_t e = left < kChunk ? uint32_t(left) : uint32_t(kChunk);
+    const uint64_t len = v.n - ch * kChunk < kChunk ? v.n - ch * kChunk : kChunk;
+    uint64_t from = e0;
     // a long list: drop what lies before the row, a block-wide probe at a
     // time (positions ascend)
-    while (e1 - e0 > 4ull * nthr) {
-      const uint64_t step = (e1 - e0 + nthr - 1) / nthr;
-      const uint64_t at = e0 + step * (tid + 1) - 1;  // the last of this thread's part
+    while (e1 - from > 4ull * nthr) {
+      const uint64_t step = (e1 - from + nthr - 1) / nthr;
+      const uint64_t at = from + step * (tid + 1) - 1;  // the last of this thread's part
       const uint32_t before = __syncthreads_count(at < e1 && v.exc_pos[at] < b);
       if (before == 0) break;
-      e0 += step * before;
+      from += step * before;
     }
-    for (uint64_t i = e0 + tid; i < e1; i += nthr) {
-      const uint32_t pos = v.exc_pos[i];
-      if (pos >= e) {
+    for (uint64_t i = from + tid; i < e1; i += nthr) {
+      const bool early = ch == ch0 && i == e0 + tid;  // read beside the row
+      const uint32_t at = early ? pos : v.exc_pos[i];
+      if (at >= e) {
         // past the row: nothing further on in a valid container
-        const uint64_t len = v.n - ch * kChunk < kChunk ? v.n - ch * kChunk : kChunk;
-        if (pos >= len) report(p.status, WC_ERR_CORRUPT);
+        if (at >= len) report(p.status, WC_ERR_CORRUPT);
         break;
       }
-      if (pos < b) continue;
-      const uint32_t c = uint32_t(ch * kChunk + pos - f0);
-      const uint32_t bits = (uint32_t(v.exc_val[i]) << 8) | lo[c];
+      if (at < b) continue;
+      const uint32_t c = uint32_t(ch * kChunk + at - f0);
+      const uint32_t bits = ((early ? high : v.exc_val[i]) << 8) | lo[c];
       const float f = __uint_as_float(bits << 16) * p.scale;
       if (kWide) static_cast<float *>(row)[c] = f;
       else static_cast<uint16_t *>(row)[c] = uint16_t(p.scale == 1.0f ? bits : bf16_bits(f));
@@ -143,7 +175,9 @@ extern "C" int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uin
   p.scale = scale;
   p.status = d_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t thr = (K / 8 + 31) / 32 * 32;
+  uint32_t thr = (K / (8 * wc12e::kBatch) + 31) / 32 * 32;
+  if (T <= 256) thr = (K / 8 + 31) / 32 * 32;  // few rows: a piece a thread
+  if (thr < 32) thr = 32;
   if (thr > wc12e::kMaxThreads) thr = wc12e::kMaxThreads;
   const bool wide = out_dtype == WC_FP32;
   if (id_bytes == 8) {

@@ -179,6 +179,8 @@ __device__ __forceinline__ void take_route(Route &r, const Route *from, uint32_t
 // ---------------------------------------------------------------------------
 constexpr uint32_t align128(uint32_t v) { return (v + 127) / 128 * 128; }
 
+// kDepth: stages of the ring
+template <uint32_t kDepth>
 struct Up {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 8 * kXRow);
   static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its list, then its sums of G_e and U_e
@@ -198,11 +200,12 @@ __device__ __forceinline__ void put_gated(uint16_t *dst, uint64_t plane, float g
 }
 
 // A stage's two subtiles: 64 rows of G_e and of U_e, the same values of H.
-__global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant__ Params p,
+template <uint32_t kDepth>
+__global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(const __grid_constant__ Params p,
                                                           const __grid_constant__ Planes planes, uint32_t csize) {
   extern __shared__ __align__(128) uint8_t dyn[];
-  Route &r = *reinterpret_cast<Route *>(dyn + Up::kRoute);
-  Bars &bars = *reinterpret_cast<Bars *>(dyn + Up::kBars);
+  Route &r = *reinterpret_cast<Route *>(dyn + Up<kDepth>::kRoute);
+  Bars &bars = *reinterpret_cast<Bars *>(dyn + Up<kDepth>::kBars);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = blockIdx.x % csize, first = blockIdx.x / csize, clusters = gridDim.x / csize;
   View v;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   }
   const uint32_t K = p.H, units = K / kUnit, u0 = units * rank / csize, u1 = units * (rank + 1) / csize;
   const uint32_t tiles = p.F / kSubRows, jobs = r.items * tiles, ring = smem_u32(dyn);
-  Turn turn;
+  Turn<kDepth> turn;
   if (warp == kWarps) {
     uint32_t s = 0;
     bool alive = true;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
           break;
         }
         uint64_t *full = &bars.full[turn.slot];
-        const uint32_t slot = ring + turn.slot * Up::kStage;
+        const uint32_t slot = ring + turn.slot * Up<kDepth>::kStage;
         if (lane == 0) {
           bar_expect(full, 2 * kSubBytes + n * 2 * kUnit);
           load_subtile(slot, planes, u * kUnit, row, full);
@@ -270,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
   offsets(next, first + clusters);
   entries(now, first);
   Exceptions x;
-  x.q = reinterpret_cast<Queues *>(dyn + Up::kQueues + warp * Up::kOwn * 4);
-  float *sums = reinterpret_cast<float *>(dyn + Up::kQueues);
+  x.q = reinterpret_cast<Queues *>(dyn + Up<kDepth>::kQueues + warp * Up<kDepth>::kOwn * 4);
+  float *sums = reinterpret_cast<float *>(dyn + Up<kDepth>::kQueues);
   const uint64_t plane = uint64_t(p.T) * p.k * p.F;
   const XAt xat = x_rows(lane);
   const uint32_t g = lane >> 2, t = lane & 3;
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
       const uint32_t most = exceptions_most(x, 2 * u);
       alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
       if (!alive) break;
-      const uint32_t slot = ring + turn.slot * Up::kStage, xs = slot + 2 * kSubBytes;
+      const uint32_t slot = ring + turn.slot * Up<kDepth>::kStage, xs = slot + 2 * kSubBytes;
       const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
       stage<1, 1, true>(gate, up, at, xat, v, x, most, K, lane);
       __syncwarp();
@@ -311,12 +314,12 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
       continue;
     }
     __syncwarp();
-    put_sums<1>(sums + warp * Up::kOwn, gate, lane);
-    put_sums<1>(sums + warp * Up::kOwn + 8 * kRedTok, up, lane);
+    put_sums<1>(sums + warp * Up<kDepth>::kOwn, gate, lane);
+    put_sums<1>(sums + warp * Up<kDepth>::kOwn + 8 * kRedTok, up, lane);
     cluster_sync();
     for (uint32_t o = tid + rank * kConsumers; o < n * kSubRows; o += kConsumers * csize) {
       const uint32_t row = o % kSubRows, c = o / kSubRows;
-      const float *at = sums + row / kRows * Up::kOwn + c * kRedTok + row % kRows;
+      const float *at = sums + row / kRows * Up<kDepth>::kOwn + c * kRedTok + row % kRows;
       float a = 0.0f, b = 0.0f;
       for (uint32_t i = 0; i < csize; i++) {
         a += cluster_load(at, i);
@@ -332,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_moe_up(const __grid_constant_
 // ---------------------------------------------------------------------------
 // A stage's two subtiles are successive ranges of F.
 struct Down {
+  static constexpr uint32_t kDepth = 3;
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 16 * kXRow);
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
@@ -342,6 +346,7 @@ struct Down {
 
 __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constant__ Params p,
                                                             const __grid_constant__ Planes planes, uint32_t csize) {
+  constexpr uint32_t kDepth = Down::kDepth;
   extern __shared__ __align__(128) uint8_t dyn[];
   Route &r = *reinterpret_cast<Route *>(dyn + Down::kRoute);
   Bars &bars = *reinterpret_cast<Bars *>(dyn + Down::kBars);
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   const uint32_t q0 = ok ? uint32_t(uint64_t(all) * rank / csize) : 0u, q1 = ok ? uint32_t(uint64_t(all) * (rank + 1) / csize) : 0u;
   const uint32_t first = q0 / per, st0 = q0 - first * per;  // item, stage of it
   if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
-  Turn turn;
+  Turn<kDepth> turn;
   if (warp == kWarps) {
     const uint64_t plane = uint64_t(p.T) * p.k * p.F;
     struct At {
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       }
     };
     auto subs_of = [&](uint32_t st) { return 2 * st + 1 < units ? 2u : 1u; };
-    auto weights = [&](const Turn &turn, const At &a) {
+    auto weights = [&](const Turn<kDepth> &turn, const At &a) {
       uint64_t *full = &bars.full[turn.slot];
       const uint32_t slot = ring + turn.slot * Down::kStage, subs = subs_of(a.st);
       const uint32_t row = uint32_t(r.item_e[a.item]) * p.H + n0;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       }
       __syncwarp();
     };
-    auto values = [&](const Turn &turn, const At &a) {  // lanes 0-7: the first plane, 8-15: the second
+    auto values = [&](const Turn<kDepth> &turn, const At &a) {  // lanes 0-7: the first plane, 8-15: the second
       const uint32_t i = lane & 7;
       if (lane < 16 && i < r.item_n[a.item])
         load_row(ring + turn.slot * Down::kStage + 2 * kSubBytes + lane * kXRow,
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
     }
     wait_prerequisites();
     asm volatile("fence.proxy.async.global;" ::: "memory");
-    Turn turn2;
+    Turn<kDepth> turn2;
     At at2{first, st0};
     for (uint32_t i = 0; i < s; i++, turn2.next()) {
       values(turn2, at2);
@@ -483,14 +488,17 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
 
 // the CTAs of the up product that run at once on the device, the kernels set
 // up
+template <uint32_t kDepth>
 int up_slots() {
   static DeviceSetup setup;
   return setup.get([] {
     int per_sm = 0;
-    if (cudaFuncSetAttribute(k12_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up::kSmem)) != cudaSuccess ||
+    if (!share_sm(k12_moe_route<1>) || !share_sm(k12_moe_route<2>) || !share_sm(k12_moe_route<4>) || !share_sm(k12_moe_route<8>) ||
+        !share_sm(k12_moe_route<16>) ||
+        cudaFuncSetAttribute(k12_moe_up<kDepth>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Up<kDepth>::kSmem)) != cudaSuccess ||
         cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Down::smem(kMaxTokens))) != cudaSuccess ||
         cudaFuncSetAttribute(k12_moe_down, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k12_moe_up, kThreads, Up::kSmem) != cudaSuccess)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k12_moe_up<kDepth>, kThreads, Up<kDepth>::kSmem) != cudaSuccess)
       return 0;
     return per_sm * wc12l::device_sms();
   });
@@ -522,7 +530,11 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   if (d_x == nullptr || d_logits == nullptr || d_out == nullptr || d_work == nullptr) return WC_ERR_INVALID_ARG;
   if (!aligned(d_x, 16) || !aligned(d_logits, 4) || !aligned(d_out, 4) || !aligned(d_work, 16)) return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_moe_work_bytes(T, k, F)) return WC_ERR_CAPACITY;
-  const int slots = up_slots(), sms = slots > 0 ? wc12l::device_sms() : 0;
+  // rows of H that are long enough fill a deeper ring of fewer CTAs (32 tokens,
+  // 128 experts, H 2048: 194 us with 4 stages, 214 with 3); of shorter ones
+  // more CTAs run, whose ends overlap (16 tokens, H 1024: 64 us against 76)
+  const bool deep = H >= 2048;
+  const int slots = deep ? up_slots<4>() : up_slots<3>(), sms = slots > 0 ? wc12l::device_sms() : 0;
   if (sms <= 0) return WC_ERR_CUDA;
   Params p;
   p.gate_up = static_cast<const uint8_t *>(d_gate_up);
@@ -550,15 +562,15 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     // more jobs than that, as many CTAs as run at once
     const uint32_t pairs = p.T * k, jobs = pairs * (F / kSubRows);
     uint32_t cu = 1;
-    while (cu < 8 && jobs * cu * 2 <= 4u * uint32_t(sms) && H / kUnit >= 2 * cu * kDepth) cu *= 2;
+    while (cu < 8 && jobs * cu * 2 <= 4u * uint32_t(sms) && H / kUnit >= 8 * cu) cu *= 2;
     // down: CTAs that split the items, the same
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
     uint32_t cd = 1;
-    while (cd < 16 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * kDepth) cd *= 2;
+    while (cd < 16 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * Down::kDepth) cd *= 2;
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
-        launch(k12_moe_up, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, Up::kSmem, s, true, p, up, cu) !=
+        launch(deep ? k12_moe_up<4> : k12_moe_up<3>, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, deep ? Up<4>::kSmem : Up<3>::kSmem, s, true, p, up, cu) !=
             cudaSuccess ||
         launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;

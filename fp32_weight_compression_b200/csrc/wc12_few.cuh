@@ -73,7 +73,7 @@ constexpr uint32_t kUnit = 64;       // values of K of a subtile
 constexpr uint32_t kMaxK = 1 << 16;  // a group's rows touch at most 17 chunks
 constexpr uint32_t kQueue = 16;      // exceptions a lane keeps
 constexpr uint32_t kRedTok = 18;     // floats a token's 16 sums take (padded: few bank conflicts)
-constexpr uint32_t kDepth = 3;       // stages of the ring
+constexpr uint32_t kMaxDepth = 4;    // stages of the ring, at most
 constexpr uint32_t kSpinLimit = 1u << 24;
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
@@ -216,12 +216,12 @@ __device__ __forceinline__ uint32_t shared2(uint32_t a) {
 }
 
 struct Bars {
-  uint64_t full[kDepth], empty[kDepth];
+  uint64_t full[kMaxDepth], empty[kMaxDepth];
   int failed;
 };
 // by one thread, before a barrier of the CTA
 __device__ __forceinline__ void bars_init(Bars &b) {
-  for (uint32_t i = 0; i < kDepth; i++) {
+  for (uint32_t i = 0; i < kMaxDepth; i++) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&b.full[i])) : "memory");
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&b.empty[i])), "n"(kWarps) : "memory");
   }
@@ -229,6 +229,7 @@ __device__ __forceinline__ void bars_init(Bars &b) {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 // A place in the ring: stage s is in slot s % kDepth, its turn s / kDepth.
+template <uint32_t kDepth>
 struct Turn {
   uint32_t slot = 0, parity = 0;
   __device__ __forceinline__ void next() {
@@ -263,7 +264,8 @@ __device__ __forceinline__ bool bar_wait(Bars &b, uint64_t *bar, uint32_t parity
 }
 // the loading warp, before it ends: no copy may be in flight then.  turn: the
 // place after the last of `count` stages
-__device__ __forceinline__ void finish_copies(Bars &b, Turn turn, uint32_t count, int32_t *status) {
+template <uint32_t kDepth>
+__device__ __forceinline__ void finish_copies(Bars &b, Turn<kDepth> turn, uint32_t count, int32_t *status) {
   // back to the first of the last kDepth stages (or of all)
   const uint32_t n = count < kDepth ? count : kDepth;
   for (uint32_t i = 0; i < n; i++) {
@@ -747,6 +749,15 @@ class DeviceSetup {
   int value_[64] = {};
   unsigned long long ctx_[64] = {};
 };
+
+// Lets the next kernel's CTAs onto the SMs where this one's run: an SM keeps
+// one division of its memory into L1 and shared memory while it has any CTA,
+// so that a kernel which needs little shared memory would shut out one that
+// needs most of it (4 to 10 us late for half of its CTAs).
+template <class Kernel>
+bool share_sm(Kernel kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+}
 
 // Launches a kernel in clusters of `cluster` CTAs along x; dependent: it may start while the kernel before it in the stream runs
 // (it waits with wait_prerequisites).
