@@ -332,18 +332,6 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
   if (csize > 1) cluster_sync();  // the others' sums are read until here
 }
 
-// the device's SMs, the kernels set up
-int device_sms() {
-  static DeviceSetup setup;
-  return setup.get([] {
-    return cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) == cudaSuccess &&
-                   share_sm(k12_adapter_shrink<1>) &&
-                   cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) ==
-                       cudaSuccess
-               ? wc12l::device_sms() : 0;
-  });
-}
-
 template <int NT>
 int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   using F = Few<NT>;
@@ -368,6 +356,7 @@ int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
 // takes 16 rows of N and 32 tokens; t enters as three bf16 numbers.
 __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __grid_constant__ Params p) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  launch_dependents();  // the shared product, which adds to Y at its end only
   const uint32_t n0 = (blockIdx.y * kSideWarps + warp) * kRows, m0 = 32 * blockIdx.x;
   int32_t ad = m0 + lane < p.M ? p.adapter[m0 + lane] : -1;
   if (ad < 0 || ad >= int32_t(p.L)) ad = -1;
@@ -426,6 +415,18 @@ __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __gr
     }
     put(c, same);
   }
+}
+
+// the device's SMs, the kernels set up
+int device_sms() {
+  static DeviceSetup setup;
+  return setup.get([] {
+    return cudaFuncSetAttribute(k12_few_adapters<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<1>::kSmem)) == cudaSuccess &&
+                   share_sm(k12_adapter_shrink<1>) && share_sm(k12_adapter_shrink<4>) && share_sm(k12_adapter_expand) &&
+                   cudaFuncSetAttribute(k12_few_adapters<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Few<2>::kSmem)) ==
+                       cudaSuccess
+               ? wc12l::device_sms() : 0;
+  });
 }
 
 }  // namespace wc12a

@@ -131,6 +131,9 @@ __host__ __device__ inline uint32_t smem_bytes(uint32_t n_mma, uint32_t depth, u
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
 
+// waits for the kernel before, if this one was launched to start beside it
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) k12_linear(const __grid_constant_
   }
   if (!ok || s_begin >= s_end) {
     if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) report(p.status, WC_ERR_CORRUPT);
+    wait_prerequisites();
     return;
   }
   const uint32_t nst = s_end - s_begin;
@@ -653,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) k12_linear(const __grid_constant_
   done = __syncthreads_and(done) != 0;
   if (!done && tid == kExpThreads) report(p.status, WC_ERR_TIMEOUT);
   fence_after_sync();
+  wait_prerequisites();  // Y, where an earlier kernel of the layer with adapters writes it
   if (done && !*flag && expander) {
     // warp w reads TMEM lanes 32 (w % 4) .. (its rows); warps 0-3 take the
     // even 8-column groups, warps 4-7 the odd ones
@@ -902,9 +907,20 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
     p.splits = (stages + p.per_split - 1) / p.per_split;
     p.add = add || p.splits > 1;
     if (p.splits > 1 && !add) wc12l::k12_zero<<<unsigned(2 * di.sms), 256, 0, s>>>(p.y, uint64_t(m) * N);
-    dim3 grid(blocks, p.splits);
-    wc12l::kernel_for(shape)<<<grid, wc12l::kThreads, smem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
+    // with add Y is being written by the kernel launched just before, which
+    // this one may start beside: it needs Y at its end only
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(blocks, p.splits);
+    c.blockDim = dim3(wc12l::kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = add && t0 == 0 ? 1 : 0;
+    if (cudaGetLastError() != cudaSuccess || cudaLaunchKernelEx(&c, wc12l::kernel_for(shape), p) != cudaSuccess)
+      return WC_ERR_CUDA;
   }
   return WC_OK;
 }

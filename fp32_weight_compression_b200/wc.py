@@ -698,7 +698,7 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     if other is not None:
         with other:
             return split12_linear_adapters(cont, N, K, x, adapter, a, b, scales, plan, out, status)
-    if x.dim() != 2 or a.dim() != 3:
+    if not isinstance(x, torch.Tensor) or not isinstance(a, torch.Tensor) or x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be M x K and a L x r x K")
     M, (L, r, _k) = x.shape[0], a.shape
     x = _want("x", x, torch.bfloat16, (M, K), dev)
@@ -740,7 +740,7 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
             return split12_moe(gate_up, down, E, H, F, x, logits, k, renormalize, dtype, out, status)
     if _container("down", down) != dev:
         raise ValueError(f"down must be on the container's device, {dev}")
-    if x.dim() != 2:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be T x H")
     T = x.shape[0]
     x = _want("x", x, torch.bfloat16, (T, H), dev)
