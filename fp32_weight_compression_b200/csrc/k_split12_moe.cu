@@ -566,7 +566,10 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     // down: CTAs that split the items, the same
     const uint32_t some = (pairs < E ? pairs : E) * (F / kUnit);  // units of a row, about
     uint32_t cd = 1;
-    while (cd < 16 && H / kSubRows * cd * 2 <= 3u * uint32_t(sms) && some >= 4 * cd * Down::kDepth) cd *= 2;
+    while (cd < 8 && H / kSubRows * (cd + 1) <= 3u * uint32_t(sms) && some >= 6 * (cd + 1)) cd++;
+    // (clusters of 9 to 15 find no room beside one another: 32 tokens, 128
+    // experts 203 -> 213 us)
+    if (cd == 8 && H / kSubRows * 16 <= 3u * uint32_t(sms) && some >= 96) cd = 16;
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
