@@ -602,20 +602,20 @@ def check_status(status: torch.Tensor, what: str = "device status") -> None:
     _check(int(status.item()), what)
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _elsewhere(device: torch.device, stream):
-    """The context to allocate and launch in, or None where that is the
-    current one: the tensors' device, the stream given."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream)
-    if torch._C._cuda_getDevice() != device.index:
+    """The context to allocate and launch in: the stream given, or the
+    tensors' device."""
+    if stream is None:
         return torch.cuda.device(device)
-    return None
+    if stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+# The checks below are written out in each call, the common case first: they
+# are a good part of what a short call costs on the host.
+_Tensor, _U8, _I32, _I64 = torch.Tensor, torch.uint8, torch.int32, torch.int64
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def _bad(name: str, t, dtype, shape, device):
@@ -624,22 +624,22 @@ def _bad(name: str, t, dtype, shape, device):
         raise TypeError(f"{name} must be a tensor of {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on the container's device, {device}")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _want(name: str, t, dtype, shape, device) -> torch.Tensor:
     """The tensor, contiguous, if it is what the call takes."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device:
         _bad(name, t, dtype, shape, device)
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _container(name: str, t) -> torch.device:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.dim() != 1 or not t.is_contiguous():
+def _bad_container(name: str, t):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a 1-D contiguous uint8 tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    return t.device
+    raise ValueError(f"{name} must be on a CUDA device")
 
 
 def _status_word(status, device) -> torch.Tensor:
@@ -647,18 +647,15 @@ def _status_word(status, device) -> torch.Tensor:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("a captured call needs a status word of the caller's")
         return torch.zeros(1, dtype=torch.int32, device=device)
-    if not isinstance(status, torch.Tensor) or status.dtype is not torch.int32 or status.numel() != 1 or status.device != device:
-        _bad("status", status, torch.int32, (1,), device)
+    if not isinstance(status, _Tensor) or status.dtype is not _I32 or status.numel() != 1 or status.device != device:
+        _bad("status", status, _I32, (1,), device)
     return status
 
 
 def _output(out, shape, dtype, device) -> torch.Tensor:
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(out, torch.Tensor) or out.dtype is not dtype or out.shape != shape or out.device != device:
+    if not isinstance(out, _Tensor) or out.dtype is not dtype or out.shape != shape or out.device != device or \
+            not out.is_contiguous():
         _bad("out", out, dtype, shape, device)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
     return out
 
 
@@ -667,20 +664,25 @@ def split12_embed(cont: torch.Tensor, V: int, K: int, ids: torch.Tensor, scale: 
     """scale * table[ids] (bf16, or fp32) with the V x K bf16 table given as a
     Split12 container on the device (wc12_embed); ids int32 or int64 of any
     shape.  An id outside [0, V) gives a row of zeros and an error."""
-    dev = _container("cont", cont)
-    other = _elsewhere(dev, stream)
-    if other is not None:
-        with other:
+    if not isinstance(cont, _Tensor) or cont.dtype is not _U8 or cont.dim() != 1 or not cont.is_cuda or not cont.is_contiguous():
+        _bad_container("cont", cont)
+    dev = cont.device
+    if stream is not None or torch._C._cuda_getDevice() != dev.index:
+        with _elsewhere(dev, stream):
             return split12_embed(cont, V, K, ids, scale, dtype, out, status)
-    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int64, torch.int32):
-        raise TypeError("ids must be a tensor of int32 or int64")
-    if dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(ids, _Tensor) or (ids.dtype is not _I64 and ids.dtype is not _I32) or ids.device != dev:
+        _bad("ids", ids, torch.int32 if isinstance(ids, _Tensor) and ids.dtype == torch.int32 else torch.int64, None, dev)
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("the output is bf16 or fp32")
-    ids = _want("ids", ids, ids.dtype, ids.shape, dev)
-    y = _output(out, (*ids.shape, K), dtype, dev)
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
+    y = cont.new_empty((*ids.shape, K), dtype=dtype) if out is None else _output(out, (*ids.shape, K), dtype, dev)
     st = _status_word(status, dev)
-    _check((_lib or load()).wc12_embed(cont.data_ptr(), cont.numel(), V, K, ids.data_ptr(), ids.element_size(), ids.numel(),
-                                       scale, y.data_ptr(), _DT[dtype], st.data_ptr(), _raw_stream(dev)), "wc12_embed")
+    rc = (_lib or load()).wc12_embed(cont.data_ptr(), cont.numel(), V, K, ids.data_ptr(), 8 if ids.dtype is _I64 else 4, ids.numel(),
+                                     scale, y.data_ptr(), BF16 if dtype is _BF16 else FP32, st.data_ptr(),
+                                     torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        raise WCError(rc, "wc12_embed")
     if status is None:
         check_status(st, "wc12_embed (device status)")
     return y
@@ -693,33 +695,35 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     none), with W (N x K bf16) given as a Split12 container on the device
     (wc12_linear_adapters): x M x K bf16, a L x r x K and b L x N x r bf16,
     scales L fp32.  The plan serves batches of more than 16 tokens."""
-    dev = _container("cont", cont)
-    other = _elsewhere(dev, stream)
-    if other is not None:
-        with other:
+    if not isinstance(cont, _Tensor) or cont.dtype is not _U8 or cont.dim() != 1 or not cont.is_cuda or not cont.is_contiguous():
+        _bad_container("cont", cont)
+    dev = cont.device
+    if stream is not None or torch._C._cuda_getDevice() != dev.index:
+        with _elsewhere(dev, stream):
             return split12_linear_adapters(cont, N, K, x, adapter, a, b, scales, plan, out, status)
-    if not isinstance(x, torch.Tensor) or not isinstance(a, torch.Tensor) or x.dim() != 2 or a.dim() != 3:
+    if not isinstance(x, _Tensor) or not isinstance(a, _Tensor) or x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be M x K and a L x r x K")
     M, (L, r, _k) = x.shape[0], a.shape
-    x = _want("x", x, torch.bfloat16, (M, K), dev)
-    adapter = _want("adapter", adapter, torch.int32, (M,), dev)
-    a = _want("a", a, torch.bfloat16, (L, r, K), dev)
-    b = _want("b", b, torch.bfloat16, (L, N, r), dev)
-    scales = _want("scales", scales, torch.float32, (L,), dev)
-    plan_ptr = plan_bytes = 0
+    x = _want("x", x, _BF16, (M, K), dev)
+    adapter = _want("adapter", adapter, _I32, (M,), dev)
+    a = _want("a", a, _BF16, (L, r, K), dev)
+    b = _want("b", b, _BF16, (L, N, r), dev)
+    scales = _want("scales", scales, _F32, (L,), dev)
+    plan_ptr, plan_bytes = None, 0
     if plan is not None:
-        if _container("plan", plan) != dev:
-            raise ValueError(f"plan must be on the container's device, {dev}")
+        if not isinstance(plan, _Tensor) or plan.dtype is not _U8 or plan.dim() != 1 or plan.device != dev or not plan.is_contiguous():
+            _bad_container("plan", plan) if not isinstance(plan, _Tensor) or plan.device == dev else _bad("plan", plan, _U8, None, dev)
         plan_ptr, plan_bytes = plan.data_ptr(), plan.numel()
-    y = _output(out, (M, N), torch.float32, dev)
-    st = _status_word(status, dev)
     lib = _lib or load()
+    y = cont.new_empty((M, N), dtype=_F32) if out is None else _output(out, (M, N), _F32, dev)
+    st = _status_word(status, dev)
     work_bytes = lib.wc12_linear_adapters_work_bytes(M, r)
-    work = torch.empty(work_bytes, dtype=torch.uint8, device=dev)
-    _check(lib.wc12_linear_adapters(
-        cont.data_ptr(), cont.numel(), plan_ptr or None, plan_bytes, N, K, x.data_ptr(), M, adapter.data_ptr(), a.data_ptr(),
-        b.data_ptr(), scales.data_ptr(), L, r, y.data_ptr(), work.data_ptr(), work_bytes, st.data_ptr(), _raw_stream(dev)),
-        "wc12_linear_adapters")
+    work = cont.new_empty(work_bytes)
+    rc = lib.wc12_linear_adapters(cont.data_ptr(), cont.numel(), plan_ptr, plan_bytes, N, K, x.data_ptr(), M, adapter.data_ptr(),
+                                  a.data_ptr(), b.data_ptr(), scales.data_ptr(), L, r, y.data_ptr(), work.data_ptr(), work_bytes,
+                                  st.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        raise WCError(rc, "wc12_linear_adapters")
     if status is None:
         check_status(st, "wc12_linear_adapters (device status)")
     return y
@@ -733,28 +737,32 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
     two Split12 containers on the device, gate_up E x 2F x H and down
     E x H x F (wc12_moe): the k experts with the largest logits, their softmax
     (over themselves, or without renormalize over all experts), SiLU-gated."""
-    dev = _container("gate_up", gate_up)
-    other = _elsewhere(dev, stream)
-    if other is not None:
-        with other:
+    if not isinstance(gate_up, _Tensor) or gate_up.dtype is not _U8 or gate_up.dim() != 1 or not gate_up.is_cuda or \
+            not gate_up.is_contiguous():
+        _bad_container("gate_up", gate_up)
+    dev = gate_up.device
+    if stream is not None or torch._C._cuda_getDevice() != dev.index:
+        with _elsewhere(dev, stream):
             return split12_moe(gate_up, down, E, H, F, x, logits, k, renormalize, dtype, out, status)
-    if _container("down", down) != dev:
-        raise ValueError(f"down must be on the container's device, {dev}")
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+    if not isinstance(down, _Tensor) or down.dtype is not _U8 or down.dim() != 1 or down.device != dev or not down.is_contiguous():
+        _bad_container("down", down) if not isinstance(down, _Tensor) or down.device == dev else _bad("down", down, _U8, None, dev)
+    if not isinstance(x, _Tensor) or x.dim() != 2:
         raise ValueError("x must be T x H")
     T = x.shape[0]
-    x = _want("x", x, torch.bfloat16, (T, H), dev)
-    logits = _want("logits", logits, torch.float32, (T, E), dev)
-    if dtype not in (torch.bfloat16, torch.float32):
+    x = _want("x", x, _BF16, (T, H), dev)
+    logits = _want("logits", logits, _F32, (T, E), dev)
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("the output is bf16 or fp32")
     lib = _lib or load()
-    y = _output(out, (T, H), dtype, dev)
+    y = gate_up.new_empty((T, H), dtype=dtype) if out is None else _output(out, (T, H), dtype, dev)
     st = _status_word(status, dev)
     work_bytes = lib.wc12_moe_work_bytes(T, k, F)
-    work = torch.empty(work_bytes, dtype=torch.uint8, device=dev)
-    _check(lib.wc12_moe(gate_up.data_ptr(), gate_up.numel(), down.data_ptr(), down.numel(), E, H, F, x.data_ptr(),
-                        logits.data_ptr(), T, k, 1 if renormalize else 0, y.data_ptr(), _DT[dtype], work.data_ptr(), work_bytes,
-                        st.data_ptr(), _raw_stream(dev)), "wc12_moe")
+    work = gate_up.new_empty(work_bytes)
+    rc = lib.wc12_moe(gate_up.data_ptr(), gate_up.numel(), down.data_ptr(), down.numel(), E, H, F, x.data_ptr(), logits.data_ptr(),
+                      T, k, 1 if renormalize else 0, y.data_ptr(), BF16 if dtype is _BF16 else FP32, work.data_ptr(), work_bytes,
+                      st.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        raise WCError(rc, "wc12_moe")
     if status is None:
         check_status(st, "wc12_moe (device status)")
     return y
