@@ -19,6 +19,11 @@
 //     D_e of every item as through one long row, whose parts its CTAs take.
 //     The weighted sum over experts is part of the product's sum: no atomics,
 //     one rounding, one write.
+// Times: 1 token, 8 of 64 experts of 2048 x 768: 29 us (57 MB); 5 tokens, 2 of
+// 8, 4096 x 1792: 54 (200 MB); 16 tokens, 4 of 32, 1024 x 1408: 64 (180 MB); 32
+// tokens, 8 of 128, 2048 x 768: 202 (790 MB, 3.9 TB/s; the up product alone
+// reads 631 MB in 113 us, 5.6 TB/s).
+//
 // k12_moe_route finds the experts first, a warp a token.  Each kernel starts
 // while the one before it ends (programmatic dependent launch); the down
 // product's has its route, exceptions and first weights by the time that the
