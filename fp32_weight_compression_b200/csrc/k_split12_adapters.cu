@@ -10,8 +10,8 @@
 //   * few tokens (kFewTokens): one kernel streams W through registers
 //     (wc12_few.cuh), waits for t only when its sums are done, and adds t B^T
 //     to them.  The kernel that makes t runs beside it (programmatic dependent
-//     launch).  4096 x 4096, 1 token: 10.3 us (25 MB); 4096 x 14336, 7 tokens:
-//     25.7 (90 MB); 14336 x 4096, 16 tokens: 34 (99 MB), where the tensor-
+//     launch).  4096 x 4096, 1 token: 10.3 us (25 MB, from L2); 4096 x 14336,
+//     7 tokens: 25.3 (90 MB); 14336 x 4096, 16 tokens: 33 (99 MB), where the tensor-
 //     memory kernel takes 36.5 for the shared product alone;
 //   * more: Y starts as the adapters' part, from a tensor-core product of t
 //     (as the sum of three bf16 numbers) and B, and the tensor-memory kernel
@@ -199,7 +199,7 @@ template <int NT>
 struct Few {
   static constexpr uint32_t kXBox = NT * 1024;  // 8 NT tokens' values of a unit
   static constexpr uint32_t kStage = 2 * kSubBytes + 2 * kXBox;
-  static constexpr uint32_t kOwn = own_words(8 * NT);  // words of a warp: its list, then its sums
+  static constexpr uint32_t kOwn = own_words(8 * NT);  // words of a warp: its queues, then its sums
   static constexpr uint32_t kQueues = kDepth * kStage;
   static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
   static constexpr uint32_t kSmem = 1024 + kBars + sizeof(Bars);  // 1024: the boxes' swizzle counts from there
@@ -238,7 +238,11 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
       __syncwarp();
     };
     uint32_t u = u0;
-    for (uint32_t i = 0; i < kDepth && u < u1; i++, u += 2, turn.next()) load(u);
+    load(u);
+    u += 2;
+    turn.next();
+    if (bar_wait(bars, &bars.asked, 0, false, p.status))
+      for (uint32_t i = 1; i < kDepth && u < u1; i++, u += 2, turn.next()) load(u);
     ok = open_header(v, p.w, p.w_bytes);  // the same for every thread
     // B's rows for the tokens' adapters, on their way to L2 for the end
     if (lane < p.M) {
@@ -260,9 +264,11 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
     exceptions_reset(x, lane);
     ok = open_header(v, p.w, p.w_bytes);
     float tot0[NT][4] = {}, tot1[NT][4] = {};
+    if (ok && v.ne > 0) window_entries(win, v, lane);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&bars.asked);
     if (ok) {
       if (v.ne > 0) {
-        window_entries(win, v, lane);
         window_keep(x, win, v, row0, K, u0, u1, 1, 0, lane, p.status);
         exceptions_ready(x, lane);
       }

@@ -19,9 +19,9 @@
 //     D_e of every item as through one long row, whose parts its CTAs take.
 //     The weighted sum over experts is part of the product's sum: no atomics,
 //     one rounding, one write.
-// Times: 1 token, 8 of 64 experts of 2048 x 768: 29 us (57 MB); 5 tokens, 2 of
-// 8, 4096 x 1792: 54 (200 MB); 16 tokens, 4 of 32, 1024 x 1408: 64 (180 MB); 32
-// tokens, 8 of 128, 2048 x 768: 202 (790 MB, 3.9 TB/s; the up product alone
+// Times: 1 token, 8 of 64 experts of 2048 x 768: 28 us (57 MB); 5 tokens, 2 of
+// 8, 4096 x 1792: 54 (200 MB); 16 tokens, 4 of 32, 1024 x 1408: 63 (180 MB); 32
+// tokens, 8 of 128, 2048 x 768: 200 (790 MB, 3.9 TB/s; the up product alone
 // reads 631 MB in 113 us, 5.6 TB/s).
 //
 // k12_moe_route finds the experts first, a warp a token.  Each kernel starts
@@ -74,7 +74,10 @@ constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_key(-inf)
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
 // Finds the experts: one CTA, a warp a token, whose lanes hold kPer logits
-// each.
+// each.  Latency bounds it (two reductions a choice): 4 us for one token and 8
+// choices, before which the up product's CTAs have started.  In the up
+// product's CTAs, each for itself, it took 9,000 cycles for one token and
+// 54,000 for 32.
 template <int kPer>
 __global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_constant__ Params p) {
   launch_dependents();
@@ -188,7 +191,7 @@ constexpr uint32_t align128(uint32_t v) { return (v + 127) / 128 * 128; }
 template <uint32_t kDepth>
 struct Up {
   static constexpr uint32_t kStage = align128(2 * kSubBytes + 8 * kXRow);
-  static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its list, then its sums of G_e and U_e
+  static constexpr uint32_t kOwn = own_words(16);  // words of a warp: its queues, then its sums of G_e and U_e
   static constexpr uint32_t kRoute = kDepth * kStage;
   static constexpr uint32_t kQueues = align128(kRoute + uint32_t(sizeof(Route)));
   static constexpr uint32_t kBars = kQueues + kWarps * kOwn * 4;
@@ -237,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
       const uint16_t *px = p.x;
       if (lane < n) px += uint64_t(r.pair[r.item_first[item] + lane] / p.k) * K;
       for (uint32_t u = u0; u < u1; u++, s++, turn.next()) {
-        if (s >= kDepth && !bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) {
+        if ((s >= kDepth && !bar_wait(bars, &bars.empty[turn.slot], turn.parity ^ 1, true, p.status)) ||
+            (s == 1 && !bar_wait(bars, &bars.asked, 0, true, p.status))) {
           alive = false;
           break;
         }
@@ -277,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
   offsets(now, first);
   offsets(next, first + clusters);
   entries(now, first);
+  __syncwarp();
+  if (lane == 0) bar_arrive(&bars.asked);
   Exceptions x;
   x.q = reinterpret_cast<Queues *>(dyn + Up<kDepth>::kQueues + warp * Up<kDepth>::kOwn * 4);
   float *sums = reinterpret_cast<float *>(dyn + Up<kDepth>::kQueues);
@@ -536,7 +542,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   if (!aligned(d_x, 16) || !aligned(d_logits, 4) || !aligned(d_out, 4) || !aligned(d_work, 16)) return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_moe_work_bytes(T, k, F)) return WC_ERR_CAPACITY;
   // rows of H that are long enough fill a deeper ring of fewer CTAs (32 tokens,
-  // 128 experts, H 2048: 194 us with 4 stages, 214 with 3); of shorter ones
+  // 128 experts, H 2048: 200 us with 4 stages, 216 with 3); of shorter ones
   // more CTAs run, whose ends overlap (16 tokens, H 1024: 64 us against 76)
   const bool deep = H >= 2048;
   const int slots = deep ? up_slots<4>() : up_slots<3>(), sms = slots > 0 ? wc12l::device_sms() : 0;

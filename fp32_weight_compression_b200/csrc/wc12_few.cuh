@@ -27,8 +27,8 @@
 // What bounds it: the expansion's instructions (see high8) and, in short rows,
 // what comes before the first stage and after the last (header, exceptions,
 // joining the parts of K: 4 to 6 us), not the memory.  14336 x 4096, 16
-// tokens, adapters of rank 16 (98.6 MB): 34 us, 2.9 TB/s, where the boxes
-// alone stream in 17.  Ways that were left: loads into registers (57 us: the
+// tokens, adapters of rank 16 (98.6 MB): 33 us, 3.0 TB/s, where the boxes
+// alone stream in 17, and the kernel without products and exceptions takes 23.  Ways that were left: loads into registers (57 us: the
 // tokens' values came from L2 at the moment of use); copies by cp.async, a
 // lane its own pieces (56: twice the product's instructions); eight warps a
 // CTA with a subtile each (64: half the independent products a lane has,
@@ -224,6 +224,12 @@ __device__ __forceinline__ uint32_t shared2(uint32_t a) {
 
 struct Bars {
   uint64_t full[kMaxDepth], empty[kMaxDepth];
+  // The multiplying warps have asked for their first exceptions: the loading
+  // warp fills the ring beyond its first stage after that, since those few
+  // bytes would otherwise wait behind 20 MB of other CTAs' stages, and the
+  // products for them (14336 x 4096, 16 tokens: 34.1 -> 32.7 us; 32 tokens
+  // through 128 experts 202 -> 200).
+  uint64_t asked;
   int failed;
 };
 // by one thread, before a barrier of the CTA
@@ -232,6 +238,7 @@ __device__ __forceinline__ void bars_init(Bars &b) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&b.full[i])) : "memory");
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&b.empty[i])), "n"(kWarps) : "memory");
   }
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&b.asked)), "n"(kWarps) : "memory");
   b.failed = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
