@@ -193,8 +193,8 @@ WC_API int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uint32_
  *                 aligned, for this call alone until it is done
  *   d_status      as for wc12_linear; WC_ERR_INVALID_ARG for an adapter
  *                 outside [-1, L), whose token gets the shared product only
- * K at most 65536, N below 2^22.  Up to 16 tokens the result is the same bits every time;
- * beyond, as for wc12_linear, sums of parts of K are added in any order.
+ * K at most 65536, N below 2^22.  Up to 16 tokens the result is the same bits
+ * every time; beyond, as for wc12_linear, sums of parts of K are added in any order.
  * Two launches up to 16 tokens, then three and more (a token slice each).
  * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY (work_bytes too small)
  * or WC_ERR_CUDA. */
@@ -219,15 +219,16 @@ WC_API int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const voi
  *   E, H, F, k    1 <= k <= E <= 512, k <= 16; H and F multiples of 64, at most
  *                 65536
  *   d_x           T x H bf16, 16-byte aligned; d_logits T x E fp32
- *   d_out         T x H, WC_BF16 (rounded once) or WC_FP32 (the gated values
- *                 enter the down product with 16 bits: off by 2^-18 of each)
+ *   d_out         T x H, 4-byte aligned; WC_BF16 (rounded once) or WC_FP32 (the
+ *                 gated values enter the down product with 16 bits: off by
+ *                 2^-18 of each)
  *   d_work        wc12_moe_work_bytes(T, k, F) bytes, 16-byte aligned, for this
  *                 call alone until it is done
  *   d_status      device i32 set to 0 by the caller: WC_ERR_CORRUPT for a bad
  *                 container
  * A token whose logits are all -inf gets zeros; one with a NaN or +inf among
  * them a row of NaN.  A token's row does not depend on the other tokens'
- * values.  Two launches for each 32 tokens; the same bits every time.  T = 0
+ * values.  Three launches for each 32 tokens; the same bits every time.  T = 0
  * does nothing.  Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
  * (work_bytes too small) or WC_ERR_CUDA. */
 WC_API uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F);
