@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
     if (ok) {
       if (v.ne > 0) {
         window_keep(x, win, v, row0, K, u0, u1, 1, 0, lane, p.status);
-        exceptions_ready(x, lane);
+        exceptions_ready(x, u0, u1, lane);
       }
       const XAt xat = x_boxes(lane);
       Turn<kDepth> turn;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 4) k12_few_adapters(const __grid_con
         if (!bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status)) break;
         const uint32_t slot = ring + turn.slot * F::kStage, xs = slot + 2 * kSubBytes;
         const StageAt at{slot, warp, xs, xs + F::kXBox, 1024, u + 1 == u1, u, u, u + 1, row0, row0};
-        stage<NT, 1, false>(tot0, tot1, at, xat, v, x, most, K, lane);
+        stage<NT, 1, false, true>(tot0, tot1, at, xat, v, x, most, K, lane, p.status);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
     if (v.ne > 0) {
 #pragma unroll 1
       for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
-      exceptions_ready(x, lane);
+      exceptions_ready(x, u0, u1, lane);
     }
     now[0] = next[0];
     now[1] = next[1];
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
       if (!alive) break;
       const uint32_t slot = ring + turn.slot * Up<kDepth>::kStage, xs = slot + 2 * kSubBytes;
       const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
-      stage<1, 1, true>(gate, up, at, xat, v, x, most, K, lane);
+      stage<1, 1, true, false>(gate, up, at, xat, v, x, most, K, lane, p.status);
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
     }
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
       exceptions_reset(x, lane);
       if (v.ne > 0) {
         window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
-        exceptions_ready(x, lane);
+        exceptions_ready(x, 2 * st, 2 * end, lane);
       }
       now = next;
       entries(now, item + 1);
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
         if (!alive) break;
         const uint32_t slot = ring + turn.slot * Down::kStage, xs = slot + 2 * kSubBytes, u = 2 * st;
         const StageAt at{slot, warp, xs, xs + 2 * kUnit, 8 * kXRow, u + 1 == units, u, u, u + 1, row_of(item), row_of(item)};
-        stage<1, 2, false>(tot0, tot1, at, xat, v, x, most, K, lane);
+        stage<1, 2, false, false>(tot0, tot1, at, xat, v, x, most, K, lane, p.status);
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
       }

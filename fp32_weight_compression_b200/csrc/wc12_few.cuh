@@ -46,8 +46,8 @@
 // in flight (or the ones of the rows before), and gives those of its part of
 // K to the lanes that will hold their values, each of which has a short
 // queue.  The products take a lane's next entry in passing, without a branch.
-// More than a queue holds: each lane's values are looked up in the
-// container's sorted lists instead (slow, and right for any container).
+// More than a queue holds: the queues are filled again on the way, or each lane's
+// values are looked up in the container's sorted lists (see stage_product_slow).
 #pragma once
 
 #include <cstdint>
@@ -121,6 +121,7 @@ __device__ __forceinline__ float cluster_load(const float *p, uint32_t rank) {
 
 // A container opened for a rows x K matrix.
 struct View {
+  const uint8_t *w;
   const uint8_t *idx, *lo;  // planes
   const uint64_t *exc_off;
   const uint16_t *exc_pos;
@@ -137,6 +138,7 @@ struct View {
 // number of values only.
 __device__ __forceinline__ void open_planes(View &v, const uint8_t *w, uint64_t n) {
   const wc12::Lay L = wc12::lay(n, 0);
+  v.w = w;
   v.n = n;
   v.exc_off = reinterpret_cast<const uint64_t *>(w + wc12::kExcOffOff);
   v.exc_pos = reinterpret_cast<const uint16_t *>(w + L.off_exc);
@@ -164,6 +166,16 @@ __device__ __forceinline__ bool open_header(View &v, const uint8_t *w, uint64_t 
            v.book.y == v.base4 + 0x07060504u && v.book.z == (v.book.x | 0x80808080u) && v.book.w == (v.book.y | 0x80808080u);
   return q1.y == uint32_t(L.nc) && q2.x == L.off_idx && q2.y == L.off_lo && q3.x == L.off_exc && q3.y == L.total &&
          L.total <= w_bytes;
+}
+
+// ---------------------------------------------------------------------------
+// The exceptions' lists of a container whose header was found to be right,
+// again: code that runs rarely gets its few values from there, and the
+// products keep none of them in registers.
+__device__ __forceinline__ void open_lists(View &v, const uint8_t *w, uint64_t n) {
+  open_planes(v, w, n);
+  v.ne = *reinterpret_cast<const uint64_t *>(w + 24);
+  v.exc_val = w + wc12::lay(n, v.ne).off_excval;
 }
 
 // ---------------------------------------------------------------------------
@@ -204,6 +216,7 @@ __device__ __forceinline__ uint2 shared8(uint32_t a) {
 // A warp's own part of shared memory: its lanes' queues, then its sums.
 struct Queues {
   uint32_t count[32];
+  uint32_t until, end;  // refilled queues: the unit that they go up to, the last one's end
   uint16_t entry[kQueue][32];
   uint8_t high[kQueue][32];
 };
@@ -371,6 +384,7 @@ __device__ __forceinline__ void mma_first(float *d, const uint32_t *a, uint32_t 
 // 5-15), which of the lane's 8 sets of 4 values there (2 step + row half;
 // bits 2-4), which value of the set (0-1).
 constexpr uint32_t kNever = 0x7FFFFFFFu;  // the set of no entry
+constexpr uint32_t kTooMany = 0x40000000u;
 // the byte `high` (in bits 16-23) into place `entry` & 3 of four
 __device__ __forceinline__ uint32_t put_high(uint32_t hi4, uint32_t entry) {
   const uint32_t i = 4 * (entry & 3u);
@@ -409,13 +423,15 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
 // A lane's exceptions, ascending: the next kOut of its queue are out, each as
 // its set (entry >> 2, kNever for none) and the entry with its high byte in
 // bits 16-23.  more: the n-entry queue of some lane of the warp has others, from
-// i on.  walk (the same for the warp): too many, look them up.
+// i on.  short_of (the same for the warp): the queues are too short for the
+// exceptions of all units, which are looked up, or the queues are filled again
+// on the way.
 constexpr int kOut = 4;
 struct Exceptions {
   Queues *q;
   uint32_t n, i;
   uint32_t set[kOut], entry[kOut];
-  bool more, walk;
+  bool more, short_of;
 };
 // Entries have come: keeps those of the group's units [u0, u1), as of
 // subtile mul * unit + plus.
@@ -427,17 +443,19 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
     if (lane == 0) report(status, WC_ERR_CORRUPT);
     return;
   }
-  if (e1 - e0 > 1u << 14) x.walk = true;
-  if (x.walk) return;
+  if (e1 - e0 > 1u << 14) {  // too many to go through them
+    x.q->count[lane] = kTooMany;
+    return;
+  }
   const uint64_t f0 = row0 * K, c0 = f0 / kChunk;
   const uint32_t chunks = window_chunks(row0, K), count = uint32_t(e1 - e0), skew = uint32_t(e0 & 1);
   const uint32_t rel = uint32_t(w.off - e0);                              // the lane's chunk's first entry
   const uint32_t begin = uint32_t(f0 - c0 * kChunk), span = kRows * K;    // of the rows, from the first chunk on
   const uint64_t left = v.n - c0 * kChunk;                                // values from the first chunk on
   const float inv = 1.0f / float(K);
-  for (uint32_t base = 0; base < count + skew; base += 64) {  // entry base - skew + 2 lane + i
-    uint32_t pos = w.pos, val = w.val;
-    if (base > 0) window_pairs(v, e0 - skew + base + 2 * lane, e1, pos, val);
+  uint32_t pos = w.pos, val = w.val, pos2 = 0, val2 = 0;
+  for (uint32_t base = 0; base < count + skew; base += 64, pos = pos2, val = val2) {  // entry base - skew + 2 lane + i
+    if (base + 64 < count + skew) window_pairs(v, e0 - skew + base + 64 + 2 * lane, e1, pos2, val2);
 #pragma unroll
     for (uint32_t i = 0; i < 2; i++) {
       const uint32_t e = base + 2 * lane + i - skew;  // wraps for the one before the first
@@ -482,36 +500,82 @@ __device__ __forceinline__ void exceptions_reset(Exceptions &x, uint32_t lane) {
     x.set[i] = kNever;
     x.entry[i] = 0;
   }
-  x.more = x.walk = false;
+  x.more = x.short_of = false;
   __syncwarp();
 }
-// all windows' entries are in the queues
-__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t lane) {
-  __syncwarp();
-  x.n = x.q->count[lane];
-  x.walk = __any_sync(0xffffffffu, x.walk || x.n > kQueue);
-  if (x.walk) x.n = 0;
+// a queue's n entries ascending
+__device__ __forceinline__ void queue_sort(Queues *q, uint32_t n, uint32_t lane) {
 #pragma unroll 1
-  for (uint32_t i = 1; i < x.n; i++) {  // a few at most: by insertion
-    const uint16_t entry = x.q->entry[i][lane];
-    const uint8_t high = x.q->high[i][lane];
+  for (uint32_t i = 1; i < n; i++) {  // a few at most: by insertion
+    const uint16_t entry = q->entry[i][lane];
+    const uint8_t high = q->high[i][lane];
     uint32_t j = i;
 #pragma unroll 1
-    for (; j > 0 && x.q->entry[j - 1][lane] > entry; j--) {
-      x.q->entry[j][lane] = x.q->entry[j - 1][lane];
-      x.q->high[j][lane] = x.q->high[j - 1][lane];
+    for (; j > 0 && q->entry[j - 1][lane] > entry; j--) {
+      q->entry[j][lane] = q->entry[j - 1][lane];
+      q->high[j][lane] = q->high[j - 1][lane];
     }
-    x.q->entry[j][lane] = entry;
-    x.q->high[j][lane] = high;
+    q->entry[j][lane] = entry;
+    q->high[j][lane] = high;
   }
+}
+// all windows' entries of units [u0, u1) are in the queues
+__device__ __forceinline__ void exceptions_ready(Exceptions &x, uint32_t u0, uint32_t u1, uint32_t lane) {
+  __syncwarp();
+  x.n = x.q->count[lane];
+  x.short_of = __any_sync(0xffffffffu, x.n > kQueue);
+  if (x.short_of) {
+    x.n = 0;
+    x.q->until = u0;  // the same by all lanes
+    x.q->end = u1;
+  }
+  queue_sort(x.q, x.n, lane);
 #pragma unroll
   for (int i = 0; i < kOut; i++) exceptions_pull(x, x.set[i], x.entry[i], lane);
   x.more = __any_sync(0xffffffffu, x.i < x.n);
 }
+// Fills the queues with the exceptions of the units from u on, of the group of
+// 16 rows from row0 on: to the last unit, or of as many (an even number) as
+// the queues hold.  until: the unit that they go up to; its highest bit: not
+// even two units' fit, so that these have to be looked up.
+static __device__ __noinline__ void queues_refill(Queues *q, const uint8_t *w12, uint64_t n, uint64_t row0, uint32_t K, uint32_t u,
+                                                  int32_t *status) {
+  const uint32_t lane = threadIdx.x & 31;
+  View v;
+  open_lists(v, w12, n);
+  Exceptions x;
+  x.q = q;
+  uint32_t span = q->end - u, mine, dense = 0;
+  for (;;) {
+    __syncwarp();
+    q->count[lane] = 0;
+    __syncwarp();
+    Window w;
+    window_offsets(w, v.exc_off, row0, K, lane);
+    window_entries(w, v, lane);
+    window_keep(x, w, v, row0, K, u, u + span, 1, 0, lane, status);
+    __syncwarp();
+    mine = q->count[lane];
+    const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
+    if (most <= kQueue) break;
+    if (span <= 2 || most >= kTooMany) {
+      mine = 0;
+      dense = 1u << 31;
+      break;
+    }
+    // as many as should fit, fewer than now
+    const uint32_t fewer = span * (kQueue - 4) / most & ~1u, least = (span - 1) & ~1u;
+    span = fewer < 2 ? 2 : fewer < least ? fewer : least;
+  }
+  q->count[lane] = mine;
+  queue_sort(q, mine, lane);
+  q->until = (u + span) | dense;
+  __syncwarp();
+}
 // How many entries a lane has at most in the stage whose first subtile is
-// key: 0, 1, 2, or 3 for more (or walk).
+// key: 0, 1, 2, or 3 for more (or where the queues are too short)
 __device__ __forceinline__ uint32_t exceptions_most(const Exceptions &x, uint32_t key) {
-  if (x.walk) return 3;
+  if (x.short_of) return 3;
   if (!__any_sync(0xffffffffu, x.set[0] - 8 * key < 16)) return 0;
   if (!__any_sync(0xffffffffu, x.set[1] - 8 * key < 16)) return 1;
   return __any_sync(0xffffffffu, x.set[2] - 8 * key < 16) ? 3 : 2;
@@ -532,22 +596,23 @@ __device__ __forceinline__ void exceptions_pass(Exceptions &x, uint32_t key, uin
 }
 // The container's exceptions among 4 values, the first at flat position f,
 // onto their high bytes.
-static __device__ __noinline__ uint32_t exceptions_walk(uint32_t hi4, const uint64_t *exc_off, const uint16_t *exc_pos,
-                                                        const uint8_t *exc_val, uint64_t ne, uint64_t f) {
+__device__ __forceinline__ uint32_t exceptions_walk(uint32_t hi4, const uint8_t *w12, uint64_t n, uint64_t f) {
+  View v;
+  open_lists(v, w12, n);
   const uint64_t c = f / kChunk;
   const uint32_t pos = uint32_t(f % kChunk);
-  uint64_t lo = exc_off[c], hi = exc_off[c + 1];
-  if (lo > hi || hi > ne) hi = lo = 0;
+  uint64_t lo = v.exc_off[c], hi = v.exc_off[c + 1];
+  if (lo > hi || hi > v.ne) hi = lo = 0;
   const uint64_t end = hi;
   while (lo < hi) {
     const uint64_t mid = (lo + hi) >> 1;
-    if (exc_pos[mid] < pos) lo = mid + 1; else hi = mid;
+    if (v.exc_pos[mid] < pos) lo = mid + 1; else hi = mid;
   }
   for (uint64_t e = lo; e < end && e < lo + 4; e++) {
-    const uint32_t p = exc_pos[e];
+    const uint32_t p = v.exc_pos[e];
     if (p < pos || p >= pos + 4) break;
     const uint32_t i = 4 * (p - pos);
-    hi4 = prmt(hi4, exc_val[e], (0x3210u & ~(0xFu << i)) | (4u << i));
+    hi4 = prmt(hi4, v.exc_val[e], (0x3210u & ~(0xFu << i)) | (4u << i));
   }
   return hi4;
 }
@@ -645,10 +710,30 @@ __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[
 }
 
 // The same for a stage with more exceptions than two a lane, a step at a time.
-template <int kTiles, int kParts, bool kShare>
+// Where the queues are too short for all units, each value is looked up in the
+// container's lists: a warp that does so takes 200 us for rows of 4096 values,
+// however few of its lanes need it.  With kRefill the queues are filled again
+// here instead, from the lists, for as many units as they hold (14336 x 4096,
+// 8 tokens, an exception in 200 values: 227 -> 67 us, one in 100: 412 -> 99).
+// The experts' kernels do without: the compiler keeps more of their loops'
+// values elsewhere with it (5 tokens, large experts 53.4 -> 56.3 us, 16 tokens
+// 63 -> 68).
+template <int kTiles, int kParts, bool kShare, bool kRefill>
 __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat,
-                                                   const View &v, const Exceptions &x, uint32_t K, uint32_t lane) {
+                                                   const View &v, Exceptions &x, uint32_t K, uint32_t lane, int32_t *status) {
   const uint32_t g = lane >> 2, t = lane & 3;
+  bool dense = !kRefill && x.short_of;
+  if (kRefill && x.short_of) {
+    if (at.unit0 >= (x.q->until & 0x7FFFFFFFu)) {
+      queues_refill(x.q, v.w, v.n, at.row0, K, at.unit0, status);
+      x.n = x.q->count[lane];
+      x.i = 0;
+#pragma unroll
+      for (int i = 0; i < kOut; i++) exceptions_pull(x, x.set[i], x.entry[i], lane);
+      x.more = __any_sync(0xffffffffu, x.i < x.n);
+    }
+    dense = x.q->until >> 31;
+  }
 #pragma unroll 1
   for (uint32_t step = 0; step < (at.only ? 4 : 8); step++) {
     const uint32_t sub = step >> 2, s = step & 3, from = at.slot + sub * kSubBytes;
@@ -660,10 +745,9 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
       uint32_t hi[2];
       high8<false>(hi, q, v.book, 0);
       uint32_t hi4 = hi[0];
-      if (x.walk) {
+      if (dense) {
         const uint64_t at_row = (sub ? at.row1 : at.row0) + g + 8 * r;
-        hi4 = exceptions_walk(hi4, v.exc_off, v.exc_pos, v.exc_val, v.ne,
-                              at_row * K + kUnit * (sub ? at.unit1 : at.unit0) + 16 * t + 4 * s);
+        hi4 = exceptions_walk(hi4, v.w, v.n, at_row * K + kUnit * (sub ? at.unit1 : at.unit0) + 16 * t + 4 * s);
       } else {
         const uint32_t set = 8 * (at.key + sub) + 2 * s + r;
 #pragma unroll
@@ -696,11 +780,11 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
 }
 
 // The one of these that the stage needs.
-template <int kTiles, int kParts, bool kShare>
+template <int kTiles, int kParts, bool kShare, bool kRefill>
 __device__ __forceinline__ void stage(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat, const View &v,
-                                      Exceptions &x, uint32_t most, uint32_t K, uint32_t lane) {
+                                      Exceptions &x, uint32_t most, uint32_t K, uint32_t lane, int32_t *status) {
   if (most == 3) {
-    stage_product_slow<kTiles, kParts, kShare>(tot0, tot1, at, xat, v, x, K, lane);
+    stage_product_slow<kTiles, kParts, kShare, kRefill>(tot0, tot1, at, xat, v, x, K, lane, status);
   } else if (v.runs) {
     if (most == 0) stage_product<kTiles, kParts, kShare, true, 0>(tot0, tot1, at, xat, v, x, lane);
     else if (most == 1) stage_product<kTiles, kParts, kShare, true, 1>(tot0, tot1, at, xat, v, x, lane);
