@@ -24,6 +24,7 @@
 
 #include "wc12_few.cuh"
 #include "wc12_plan.cuh"
+#include "wc12_ranks.cuh"
 
 namespace wc12l {
 int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t plan_bytes, uint32_t N, uint32_t K,
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __gr
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const uint32_t m = m0 + 8 * i + g;
-    pt[i] = reinterpret_cast<const uint16_t *>(p.t) + uint64_t(m < p.M ? m : p.M - 1) * p.r + 4 * t;
+    pt[i] = reinterpret_cast<const uint16_t *>(p.t) + uint64_t(m < p.M ? m : p.M - 1) * p.r;
   }
   // a token's part goes to Y as its adapter's turn comes: another adapter's
   // infinite values never meet it
@@ -401,12 +402,12 @@ __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __gr
     const int32_t cur = __shfl_sync(0xffffffffu, ad, __ffs(rest) - 1);
     const uint32_t same = __ballot_sync(0xffffffffu, ad == cur);
     rest &= ~same;
-    const uint16_t *pb = p.b + (uint64_t(cur) * p.N + n0 + g) * p.r + 4 * t;
+    const uint16_t *pb = p.b + (uint64_t(cur) * p.N + n0 + g) * p.r;
     float c[4][4] = {};
 #pragma unroll 1
     for (uint32_t j = 0; j < p.r; j += 16) {
-      const bool in = j + 4 * t < p.r;
-      const uint32_t k = in ? j : 0;
+      const bool in = has_ranks(j, t, p.r);
+      const uint32_t k = ranks_from(j, t, p.r);
       uint2 b0 = load8(pb + k), b1 = load8(pb + uint64_t(8) * p.r + k), v[4][3];
 #pragma unroll
       for (int i = 0; i < 4; i++)
