@@ -23,6 +23,9 @@ using namespace wc12f;
 
 constexpr uint32_t kMaxThreads = 256;
 constexpr uint32_t kBatch = 4;  // pieces of 8 values of a thread at once
+// A row's columns are counted with 32 bits, up to one round of the CTA's pieces
+// (8 kBatch kMaxThreads values) past its end.
+constexpr uint32_t kMaxColumns = 1u << 31;
 
 struct Params {
   const uint8_t *w;
@@ -161,7 +164,7 @@ extern "C" int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uin
                               int32_t *d_status, void *stream) {
   auto aligned = [](const void *q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; };
   if (d_w == nullptr || d_status == nullptr || !aligned(d_w, 16) || !aligned(d_status, 4)) return WC_ERR_INVALID_ARG;
-  if (V == 0 || K == 0 || K % 8 != 0 || V > wc12::kMaxN / K || w_bytes < 96) return WC_ERR_INVALID_ARG;
+  if (V == 0 || K == 0 || K % 8 != 0 || K > wc12e::kMaxColumns || V > wc12::kMaxN / K || w_bytes < 96) return WC_ERR_INVALID_ARG;
   if ((id_bytes != 4 && id_bytes != 8) || (out_dtype != WC_BF16 && out_dtype != WC_FP32)) return WC_ERR_INVALID_ARG;
   const uint64_t n = V * K;
   const wc12::Lay L = wc12::lay(n, 0);

@@ -164,7 +164,7 @@ WC_API int32_t wc12_linear_planned(const void *d_w, uint64_t w_bytes, const void
 /* Embedding lookup out of a table held as a Split12 container, only the rows
  * asked for read: out[t, :] = scale * table[ids[t], :].
  *   d_w, w_bytes  the container (16-byte aligned; as for wc12_linear), n = V * K
- *   V, K          rows of the table; K a multiple of 8
+ *   V, K          rows of the table; K a multiple of 8, at most 2^31
  *   d_ids         T row numbers, id_bytes 4 (int32) or 8 (int64) each, aligned
  *                 to their size, in any order, repeated or not
  *   scale         multiplied in fp32; with 1 a bf16 output has the table's bits
