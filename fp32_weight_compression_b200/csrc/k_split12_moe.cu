@@ -24,10 +24,12 @@
 // tokens, 8 of 128, 2048 x 768: 200 (790 MB, 3.9 TB/s; the up product alone
 // reads 631 MB in 113 us, 5.6 TB/s).
 //
-// k12_moe_route finds the experts first, a warp a token.  Each kernel starts
-// while the one before it ends (programmatic dependent launch); the down
-// product's has its route, exceptions and first weights by the time that the
-// up product is done.
+// k12_moe_route finds the experts first, a warp a token.  The up product starts
+// when that is done; the down product starts beside the up product (programmatic
+// dependent launch) and has its route, exceptions and first weights by the time
+// that hs is there.  The up product is no dependent launch itself: the down
+// product reads the route before it waits for the up product, and a kernel sees
+// before that wait only what was finished before the up product began.
 #include <cstdint>
 
 #include "wc12_few.cuh"
@@ -75,12 +77,10 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 
 // Finds the experts: one CTA, a warp a token, whose lanes hold kPer logits
 // each.  Latency bounds it (two reductions a choice): 4 us for one token and 8
-// choices, before which the up product's CTAs have started.  In the up
-// product's CTAs, each for itself, it took 9,000 cycles for one token and
-// 54,000 for 32.
+// choices.  In the up product's CTAs, each for itself, it took 9,000 cycles for
+// one token and 54,000 for 32.
 template <int kPer>
 __global__ void __launch_bounds__(32 * kMaxTokens) k12_moe_route(const __grid_constant__ Params p) {
-  launch_dependents();
   __shared__ uint32_t who[kMaxExperts];    // the tokens that chose each expert, a bit each
   __shared__ uint16_t place[kMaxExperts];  // their first place in pair[]
   Route &r = *p.route;
@@ -219,9 +219,8 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
   View v;
   open_planes(v, p.gate_up, uint64_t(p.E) * 2 * p.F * p.H);
   const bool ok = open_header(v, p.gate_up, p.gate_up_bytes);  // the same for every thread
+  launch_dependents();  // the down product's CTAs
   if (tid == 0) bars_init(bars);
-  wait_prerequisites();  // the route
-  launch_dependents();   // the down product's CTAs, which read the route too
   take_route(r, p.route, p.T * p.k);
   __syncthreads();
   if (!ok) {
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
   float *acc = reinterpret_cast<float *>(dyn + Down::kAcc) + warp * p.T * kRedTok;  // [token][row]
   if (warp < kWarps)
     for (uint32_t i = lane; i < p.T * kRedTok; i += 32) acc[i] = 0.0f;
-  take_route(r, p.route, p.T * p.k);  // the up product's CTAs had it before this one could start
+  take_route(r, p.route, p.T * p.k);  // finished before the up product, beside which this one runs, began
   __syncthreads();
   // the items' stages one after another; this CTA's: [q0, q1)
   const uint32_t K = p.F, units = K / kUnit, per = (units + 1) / 2, all = r.items * per, ring = smem_u32(dyn);
@@ -584,7 +583,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
     const uint32_t per = (E + 31) / 32;  // logits of a lane
     auto route = per <= 1 ? k12_moe_route<1> : per <= 2 ? k12_moe_route<2> : per <= 4 ? k12_moe_route<4> : per <= 8 ? k12_moe_route<8> : k12_moe_route<16>;
     if (launch(route, dim3(1), 32 * p.T, 1, 0, s, false, p) != cudaSuccess ||
-        launch(deep ? k12_moe_up<4> : k12_moe_up<3>, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, deep ? Up<4>::kSmem : Up<3>::kSmem, s, true, p, up, cu) !=
+        launch(deep ? k12_moe_up<4> : k12_moe_up<3>, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, deep ? Up<4>::kSmem : Up<3>::kSmem, s, false, p, up, cu) !=
             cudaSuccess ||
         launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
       return WC_ERR_CUDA;
