@@ -60,8 +60,14 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // a value as the sum of three bf16 numbers, exact to 2^-24 and better of its
-// size (each takes 8 bits off; truncated, so that the rest is exact in fp32)
+// size (each takes 8 bits off; truncated, so that the rest is exact in fp32);
+// what is not finite in the first alone, since infinity less infinity is none
 __device__ __forceinline__ void split3(float v, uint32_t &h0, uint32_t &h1, uint32_t &h2) {
+  if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) {
+    h0 = v != v ? 0x7FC00000u : __float_as_uint(v);  // a NaN whose upper half could read as infinity
+    h1 = h2 = 0u;
+    return;
+  }
   h0 = __float_as_uint(v) & 0xFFFF0000u;
   const float r1 = v - __uint_as_float(h0);
   h1 = __float_as_uint(r1) & 0xFFFF0000u;
