@@ -51,3 +51,22 @@ def test_infinite_scale(wc, M):  # noqa: F811
     # one sign for each token's sums, so that infinite parts agree
     a[1] = a[1][0]
     assert bool(torch.isinf(adapters(wc, w, x, ad, a, b, s)[ad == 1]).all())
+
+
+@pytest.mark.parametrize("M", [4, 16, 17, 40])
+@pytest.mark.parametrize("r", [8, 24])
+def test_infinite_b(wc, M, r):  # noqa: F811
+    """An infinite value of B makes its row's outputs infinite, with the sign
+    of the sum that it meets, though that is held in parts of which some are
+    zero and some have the other sign; so with a sum of a power of two."""
+    w, x, ad, a, b, s = adapters_case(np.random.default_rng(M + r), M, 128, 256, 3, r)
+    ad = torch.from_numpy((np.arange(M) % 4 - 1).astype(np.int32))
+    b[1, 77, 2], b[2, 0, r - 1], b[2, 127, 0] = INF, -INF, INF
+    s[2], x[:, 9] = 1.0, 2.0
+    a[2, 0], a[2, 0, 9] = 0.0, 0.5  # the first sum of adapter 2 is 1 exactly
+    want = adapters(wc, w, x, ad, a, b, s)
+    assert torch.equal(torch.isinf(want[:, 77]), ad == 1)
+    assert torch.equal(want[:, 127] == INF, ad == 2) and torch.equal(torch.isinf(want[:, 0]), ad == 2)
+    b[1, 77, 2] = float("nan")
+    want = adapters(wc, w, x, ad, a, b, s)
+    assert torch.equal(torch.isnan(want[:, 77]), ad == 1)
