@@ -74,11 +74,6 @@ __device__ __forceinline__ void split3(float v, uint32_t &h0, uint32_t &h1, uint
   h2 = __float_as_uint(r1 - __uint_as_float(h1)) & 0xFFFF0000u;
 }
 
-// two bf16 values, those that are not finite as zeros: what the lower parts of
-// a split value are multiplied by.  An infinite B times the first part is
-// infinite; times a zero or a part of the other sign it would make that NaN.
-__device__ __forceinline__ uint32_t finite2(uint32_t w) { return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
-
 // loads that stay where they are written: all of a batch before its first use
 __device__ __forceinline__ uint4 load16(const uint16_t *p) {
   uint4 v;
@@ -431,6 +426,8 @@ __global__ void __launch_bounds__(kSideThreads, 6) k12_adapter_expand(const __gr
 #pragma unroll
           for (int part = 0; part < 3; part++) v[i][part] = make_uint2(0u, 0u);
       }
+      // an infinite B times t's first part is infinite; times a lower one, a
+      // zero or of the other sign, it would make that NaN
       const uint32_t a[4] = {b0.x, b1.x, b0.y, b1.y}, low[4] = {finite2(b0.x), finite2(b1.x), finite2(b0.y), finite2(b1.y)};
 #pragma unroll
       for (int part = 2; part >= 0; part--)

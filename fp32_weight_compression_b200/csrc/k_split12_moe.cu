@@ -444,15 +444,18 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
     Exceptions x;
     x.q = reinterpret_cast<Queues *>(dyn + Down::kQueues + warp * sizeof(Queues));
     const XAt xat = x_rows(lane);
+    const bool wild = book_wild(v.book);
     uint32_t st = st0;
     bool alive = true;
     for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
       const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
       exceptions_reset(x, lane);
       if (v.ne > 0) {
-        window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
+        const bool some = window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
         exceptions_ready(x, 2 * st, 2 * end, lane);
+        x.short_of = x.short_of || __any_sync(0xffffffffu, some);
       }
+      x.short_of = x.short_of || wild;
       now = next;
       entries(now, item + 1);
       offsets(next, item + 2);

@@ -168,6 +168,15 @@ __device__ __forceinline__ bool open_header(View &v, const uint8_t *w, uint64_t 
          L.total <= w_bytes;
 }
 
+// Whether a high byte of infinities and NaN (and of values from 2^127 on) is in
+// the codebook.
+__device__ __forceinline__ bool book_wild(uint4 book) {
+  auto in = [](uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); };
+  return (in(book.x) | in(book.y) | in(book.z) | in(book.w)) != 0;
+}
+// two bf16 values, those that are not finite as zeros
+__device__ __forceinline__ uint32_t finite2(uint32_t w) { return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
+
 // ---------------------------------------------------------------------------
 // The exceptions' lists of a container whose header was found to be right,
 // again: code that runs rarely gets its few values from there, and the
@@ -425,7 +434,8 @@ __device__ __forceinline__ void window_entries(Window &w, const View &v, uint32_
 // bits 16-23.  more: the n-entry queue of some lane of the warp has others, from
 // i on.  short_of (the same for the warp): the queues are too short for the
 // exceptions of all units, which are looked up, or the queues are filled again
-// on the way.
+// on the way.  The experts' down product, whose values come in two parts, also
+// sets it where weights may be infinite: see stage_product_slow.
 constexpr int kOut = 4;
 struct Exceptions {
   Queues *q;
@@ -434,19 +444,21 @@ struct Exceptions {
   bool more, short_of;
 };
 // Entries have come: keeps those of the group's units [u0, u1), as of
-// subtile mul * unit + plus.
-__device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, const View &v, uint64_t row0, uint32_t K,
+// subtile mul * unit + plus.  Returns whether a value among this lane's entries
+// may not be finite.
+__device__ __forceinline__ bool window_keep(Exceptions &x, const Window &w, const View &v, uint64_t row0, uint32_t K,
                                             uint32_t u0, uint32_t u1, uint32_t mul, uint32_t plus, uint32_t lane, int32_t *status) {
   const uint64_t e0 = __shfl_sync(0xffffffffu, w.off, 0), e1 = __shfl_sync(0xffffffffu, w.off, 31);
   const uint64_t before = __shfl_up_sync(0xffffffffu, w.off, 1);
   if (__any_sync(0xffffffffu, (lane > 0 && w.off < before) || w.off > v.ne)) {
     if (lane == 0) report(status, WC_ERR_CORRUPT);
-    return;
+    return false;
   }
   if (e1 - e0 > 1u << 14) {  // too many to go through them
     x.q->count[lane] = kTooMany;
-    return;
+    return false;
   }
+  bool wild = false;
   const uint64_t f0 = row0 * K, c0 = f0 / kChunk;
   const uint32_t chunks = window_chunks(row0, K), count = uint32_t(e1 - e0), skew = uint32_t(e0 & 1);
   const uint32_t rel = uint32_t(w.off - e0);                              // the lane's chunk's first entry
@@ -476,9 +488,11 @@ __device__ __forceinline__ void window_keep(Exceptions &x, const Window &w, cons
           x.q->entry[at][owner] = uint16_t((mul * u + plus) << 5 | ((col >> 2) & 3u) << 3 | (row >> 3) << 2 | (col & 3u));
           x.q->high[at][owner] = uint8_t(val >> (8 * i));
         }
+        wild = wild || ((val >> (8 * i)) & 0x7Fu) == 0x7Fu;
       }
     }
   }
+  return wild;
 }
 // the queue's next entry
 __device__ __forceinline__ void exceptions_pull(Exceptions &x, uint32_t &set, uint32_t &entry, uint32_t lane) {
@@ -718,6 +732,9 @@ __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[
 // The experts' kernels do without: the compiler keeps more of their loops'
 // values elsewhere with it (5 tokens, large experts 53.4 -> 56.3 us, 16 tokens
 // 63 -> 68).
+// Weights that are not finite meet a value's first part only: times a second
+// part, which is zero or of the other sign as often as not, an infinite one
+// would turn the sum into NaN.
 template <int kTiles, int kParts, bool kShare, bool kRefill>
 __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float tot1[kTiles][4], const StageAt &at, XAt xat,
                                                    const View &v, Exceptions &x, uint32_t K, uint32_t lane, int32_t *status) {
@@ -737,7 +754,7 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
 #pragma unroll 1
   for (uint32_t step = 0; step < (at.only ? 4 : 8); step++) {
     const uint32_t sub = step >> 2, s = step & 3, from = at.slot + sub * kSubBytes;
-    uint32_t a[4];
+    uint32_t a[4], low[4];
 #pragma unroll
     for (uint32_t r = 0; r < 2; r++) {
       const uint32_t row = at.group * kRows + g + 8 * r;
@@ -766,9 +783,13 @@ __device__ __forceinline__ void stage_product_slow(float tot0[kTiles][4], float 
       float d[4] = {};
 #pragma unroll
       for (int part = 0; part < kParts; part++) {
+        if (part == 1) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) low[j] = finite2(a[j]);
+        }
         const uint2 q = shared8((!kShare && sub ? at.xs2 : at.xs) + (s & 2 ? xat.second : xat.first) + 8 * (s & 1) +
                                 (part * kTiles + i) * at.tile_bytes);
-        mma(d, a, q.x, q.y);
+        mma(d, part ? low : a, q.x, q.y);
       }
 #pragma unroll
       for (int j = 0; j < 4; j++) {

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_split12_ops import adapters_case, adapters_exact, f64, wc  # noqa: F401
+from test_gpu_split12_ops import adapters_case, adapters_exact, f64, moe_case, moe_exact, wc  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,57 @@ def test_infinite_b(wc, M, r):  # noqa: F811
     b[1, 77, 2] = float("nan")
     want = adapters(wc, w, x, ad, a, b, s)
     assert torch.equal(torch.isnan(want[:, 77]), ad == 1)
+
+
+def moe(wc, gu, dn, x, logits, k, dtype=torch.float32):  # noqa: F811
+    E, H, F = dn.shape
+    cg, cd = wc.split12_encode(gu.cuda()), wc.split12_encode(dn.cuda())
+    got = wc.split12_moe(cg, cd, E, H, F, x.cuda(), logits.cuda(), k, dtype=dtype)
+    return check_like(got, *moe_exact(gu, dn, x, logits, k, True, dtype))
+
+
+def chose(logits, k, e):
+    return (torch.topk(logits, k, dim=1).indices == e).any(1)
+
+
+@pytest.mark.parametrize("T", [1, 3, 12, 33])
+@pytest.mark.parametrize("outliers", [0.0, 0.3])
+def test_infinite_down(wc, T, outliers):  # noqa: F811
+    """An infinite weight of an expert's down product makes its output
+    infinite for the tokens that chose the expert, with the gated value's
+    sign, though that enters in two parts; few exceptions, and so many that
+    they are looked up."""
+    E, H, F, k = 5, 128, 192, 2
+    for dtype in (torch.float32, torch.bfloat16):
+        gu, dn, x, logits = moe_case(np.random.default_rng(T + int(10 * outliers)), T, E, H, F, outliers)
+        dn[1, 7, 9], dn[2, 100, 191], dn[3, 5, 0] = INF, -INF, float("nan")
+        want = moe(wc, gu, dn, x, logits, k, dtype)
+        assert torch.equal(torch.isinf(want[:, 7]), chose(logits, k, 1))
+        assert torch.equal(torch.isinf(want[:, 100]), chose(logits, k, 2))
+        assert torch.equal(torch.isnan(want[:, 5]), chose(logits, k, 3))
+
+
+def test_infinite_down_in_the_codebook(wc):  # noqa: F811
+    """The same where infinity's high byte is one of the codebook's: no
+    exception says where they are."""
+    T, E, H, F, k = 9, 3, 128, 64, 1
+    gu, dn, x, logits = moe_case(np.random.default_rng(5), T, E, H, F)
+    dn[:, :, 9] = INF
+    dn[1, :, 9] = -INF
+    head = wc.split12_encode(dn.cuda())[:80].cpu().numpy()
+    assert {0x7F, 0xFF} & set(head[64:64 + int(head[7])].tolist())
+    assert bool(torch.isinf(moe(wc, gu, dn, x, logits, k)).all())
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_infinite_gate_and_up(wc, T):  # noqa: F811
+    """Infinite weights of G and U: infinite gated values, and NaN where the
+    gate is minus infinity, for the tokens that chose the expert."""
+    E, H, F, k = 4, 64, 64, 2
+    gu, dn, x, logits = moe_case(np.random.default_rng(T), T, E, H, F)
+    gu[1, 3, 11] = INF       # G
+    gu[2, F + 60, 0] = -INF  # U
+    assert bool((dn != 0).all()) and bool((x != 0).all())
+    want = moe(wc, gu, dn, x, logits, k)
+    some = chose(logits, k, 1) | chose(logits, k, 2)
+    assert torch.equal(~torch.isfinite(want), some.unsqueeze(1).expand(T, H))
