@@ -30,6 +30,7 @@
 // that hs is there.  The up product is no dependent launch itself: the down
 // product reads the route before it waits for the up product, and a kernel sees
 // before that wait only what was finished before the up product began.
+#include <cmath>
 #include <cstdint>
 
 #include "wc12_few.cuh"
@@ -199,10 +200,12 @@ struct Up {
 };
 
 // p_e silu(gate) up as two bf16 numbers, each rounded to nearest: off by at
-// most 2^-18 of it
+// most 2^-18 of it.  A finite one that would round to infinity keeps its upper
+// half, and the rest is the second; an infinite one has no second.
 __device__ __forceinline__ void put_gated(uint16_t *dst, uint64_t plane, float gate, float up, float weight) {
   const float h = gate / (1.0f + expf(-gate)) * up * weight;
-  const uint32_t hi = bf16_bits(h);
+  uint32_t hi = bf16_bits(h);
+  if ((hi & 0x7F80u) == 0x7F80u && fabsf(h) < INFINITY) hi = __float_as_uint(h) >> 16;
   dst[0] = uint16_t(hi);
   dst[plane] = uint16_t((hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(h - __uint_as_float(hi << 16)));
 }

@@ -124,3 +124,20 @@ def test_infinite_gate_and_up(wc, T):  # noqa: F811
     want = moe(wc, gu, dn, x, logits, k)
     some = chose(logits, k, 1) | chose(logits, k, 2)
     assert torch.equal(~torch.isfinite(want), some.unsqueeze(1).expand(T, H))
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_largest_gated_values(wc, T):  # noqa: F811
+    """A gated value just below the largest fp32 number, which bf16 would
+    round to infinity: (2 - 2^-9) 2^127 = 2^64 * (2 - 2^-9) 2^63, one expert.
+    The outputs, 2^-20 times that, are finite."""
+    E, H, F = 1, 64, 64
+    gu, dn = torch.zeros(E, 2 * F, H, dtype=torch.bfloat16), torch.zeros(E, H, F, dtype=torch.bfloat16)
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    gu[0, 5, 0] = 2.0 ** 64
+    gu[0, F + 5, 0], gu[0, F + 5, 1] = (2 - 2.0 ** -7) * 2.0 ** 63, (2.0 ** -7 - 2.0 ** -9) * 2.0 ** 63
+    dn[0, :, 5] = 2.0 ** -20
+    dn[0, 1::2, 5] = -1.5 * 2.0 ** -20
+    want = moe(wc, gu, dn, x, torch.zeros(T, E), 1)
+    assert float(want.abs().min()) == (2 - 2.0 ** -9) * 2.0 ** 107
