@@ -367,7 +367,7 @@ int32_t launch_few(const Params &p, int sms, cudaStream_t s) {
   while (csize < 8 && blocks * csize * 2 <= 4u * uint32_t(sms) && units >= 4 * csize * kDepth) csize *= 2;
   return launch(k12_few_adapters<NT>, dim3(blocks * csize), kThreads, csize, F::kSmem, s, true, p, planes, tm_x, csize) ==
                  cudaSuccess
-             ? WC_OK : WC_ERR_CUDA;
+             ? WC_OK : cuda_failed();
 }
 
 // ---------------------------------------------------------------------------
@@ -473,7 +473,7 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
     return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_linear_adapters_work_bytes(M, r)) return WC_ERR_CAPACITY;
   const int sms = device_sms();
-  if (sms <= 0) return WC_ERR_CUDA;
+  if (sms <= 0) return cuda_failed();
   Params p;
   p.w = static_cast<const uint8_t *>(d_w);
   p.w_bytes = w_bytes;
@@ -500,10 +500,10 @@ extern "C" int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const
     while (csize < 8 && tiles * ranks * csize < 2u * uint32_t(sms) && K / 64 >= 4 * csize * kSideWarps) csize *= 2;
     if (launch(M <= kFewTokens ? k12_adapter_shrink<1> : k12_adapter_shrink<4>, dim3(tiles * csize, ranks, z), kSideThreads, csize, 0, s,
                false, p, csize) != cudaSuccess)
-      return WC_ERR_CUDA;
+      return cuda_failed();
   }
   if (M <= kFewTokens) return M <= 8 ? launch_few<1>(p, sms, s) : launch_few<2>(p, sms, s);
   if (launch(k12_adapter_expand, dim3((M + 31) / 32, N / (kRows * kSideWarps)), kSideThreads, 1, 0, s, true, p) != cudaSuccess)
-    return WC_ERR_CUDA;
+    return cuda_failed();
   return wc12l::linear(d_w, w_bytes, d_plan, plan_bytes, N, K, d_x, M, d_y, true, d_status, stream);
 }

@@ -864,7 +864,10 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
   p.K = K;
   p.status = d_status;
   const wc12l::DevInfo di = wc12l::dev_info();
-  if (di.sms <= 0 || !di.attr) return WC_ERR_CUDA;
+  if (di.sms <= 0 || !di.attr) {
+    cudaGetLastError();
+    return WC_ERR_CUDA;
+  }
   const uint32_t blocks = N / wc12l::kBM, stages = K / wc12l::kBK;
   if (blocks == 0) return WC_ERR_INVALID_ARG;
   if (!wc12l::make_map(&p.tm_idx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w + L.off_idx, K / 2, N, K / 2, 32,
@@ -919,8 +922,11 @@ int32_t linear(const void *d_w, uint64_t w_bytes, const void *d_plan, uint64_t p
     c.stream = s;
     c.attrs = at;
     c.numAttrs = add && t0 == 0 ? 1 : 0;
-    if (cudaGetLastError() != cudaSuccess || cudaLaunchKernelEx(&c, wc12l::kernel_for(shape), p) != cudaSuccess)
+    if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
+    if (cudaLaunchKernelEx(&c, wc12l::kernel_for(shape), p) != cudaSuccess) {
+      cudaGetLastError();  // reported here: the next call must not find it again
       return WC_ERR_CUDA;
+    }
   }
   return WC_OK;
 }

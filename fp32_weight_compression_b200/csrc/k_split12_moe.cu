@@ -551,7 +551,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   // more CTAs run, whose ends overlap (16 tokens, H 1024: 64 us against 76)
   const bool deep = H >= 2048;
   const int slots = deep ? up_slots<4>() : up_slots<3>(), sms = slots > 0 ? wc12l::device_sms() : 0;
-  if (sms <= 0) return WC_ERR_CUDA;
+  if (sms <= 0) return cuda_failed();
   Params p;
   p.gate_up = static_cast<const uint8_t *>(d_gate_up);
   p.gate_up_bytes = gate_up_bytes;
@@ -592,7 +592,7 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
         launch(deep ? k12_moe_up<4> : k12_moe_up<3>, dim3(cu > 1 ? jobs * cu : jobs < uint32_t(slots) ? jobs : uint32_t(slots)), kThreads, cu, deep ? Up<4>::kSmem : Up<3>::kSmem, s, false, p, up, cu) !=
             cudaSuccess ||
         launch(k12_moe_down, dim3(H / kSubRows * cd), kThreads, cd, Down::smem(p.T), s, true, p, down, cd) != cudaSuccess)
-      return WC_ERR_CUDA;
+      return cuda_failed();
   }
   return WC_OK;
 }

@@ -903,4 +903,11 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, uint32_t block, uint32_t 
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
+// What a call returns after a CUDA error, which it has reported then: the next
+// call's check of its own launches must not find it again.
+inline int32_t cuda_failed() {
+  cudaGetLastError();
+  return WC_ERR_CUDA;
+}
+
 }  // namespace wc12f
