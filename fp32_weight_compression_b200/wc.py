@@ -594,7 +594,10 @@ def split12_linear(cont: torch.Tensor, N: int, K: int, x: torch.Tensor, plan=Non
 # that they run on.  Without `status` they wait and raise, as the calls above
 # do; with a status word of the caller's (int32, zero at first, on the device)
 # they only queue work, so that they can be captured into a graph, and
-# check_status() raises later for all calls that shared the word.
+# check_status() raises later for all calls that shared the word.  On a stream
+# that is given, the tensors are held for it until that work is done, though the
+# caller lets go of them, and the output for the stream that is current (the
+# order between the two streams is the caller's, as with any other work).
 
 def check_status(status: torch.Tensor, what: str = "device status") -> None:
     """Raise if a status word that calls were given has been set (waits for
@@ -610,6 +613,18 @@ def _elsewhere(device: torch.device, stream):
     if stream.device != device:
         raise ValueError("the stream belongs to another device than the tensors")
     return torch.cuda.stream(stream)
+
+
+def _held(y, stream, *tensors):
+    """y; the memory of the tensors that a call on `stream` reads or writes is
+    not given away before the stream has come past it, that of y (the stream's)
+    not before the current one has."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        y.record_stream(torch.cuda.current_stream(y.device))
+    return y
 
 
 # The checks below are written out in each call, the common case first: they
@@ -669,7 +684,8 @@ def split12_embed(cont: torch.Tensor, V: int, K: int, ids: torch.Tensor, scale: 
     dev = cont.device
     if stream is not None or torch._C._cuda_getDevice() != dev.index:
         with _elsewhere(dev, stream):
-            return split12_embed(cont, V, K, ids, scale, dtype, out, status)
+            y = split12_embed(cont, V, K, ids, scale, dtype, out, status)
+        return _held(y, stream, cont, ids, out, status)
     if not isinstance(ids, _Tensor) or (ids.dtype is not _I64 and ids.dtype is not _I32) or ids.device != dev:
         _bad("ids", ids, torch.int32 if isinstance(ids, _Tensor) and ids.dtype == torch.int32 else torch.int64, None, dev)
     if dtype is not _BF16 and dtype is not _F32:
@@ -700,7 +716,8 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     dev = cont.device
     if stream is not None or torch._C._cuda_getDevice() != dev.index:
         with _elsewhere(dev, stream):
-            return split12_linear_adapters(cont, N, K, x, adapter, a, b, scales, plan, out, status)
+            y = split12_linear_adapters(cont, N, K, x, adapter, a, b, scales, plan, out, status)
+        return _held(y, stream, cont, x, adapter, a, b, scales, plan, out, status)
     if not isinstance(x, _Tensor) or not isinstance(a, _Tensor) or x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be M x K and a L x r x K")
     M, (L, r, _k) = x.shape[0], a.shape
@@ -743,7 +760,8 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
     dev = gate_up.device
     if stream is not None or torch._C._cuda_getDevice() != dev.index:
         with _elsewhere(dev, stream):
-            return split12_moe(gate_up, down, E, H, F, x, logits, k, renormalize, dtype, out, status)
+            y = split12_moe(gate_up, down, E, H, F, x, logits, k, renormalize, dtype, out, status)
+        return _held(y, stream, gate_up, down, x, logits, out, status)
     if not isinstance(down, _Tensor) or down.dtype is not _U8 or down.dim() != 1 or down.device != dev or not down.is_contiguous():
         _bad_container("down", down) if not isinstance(down, _Tensor) or down.device == dev else _bad("down", down, _U8, None, dev)
     if not isinstance(x, _Tensor) or x.dim() != 2:
