@@ -651,6 +651,11 @@ def _want(name: str, t, dtype, shape, device) -> torch.Tensor:
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _no_gradient(what: str):
+    raise ValueError(f"{what} has no backward pass, and an input requires a gradient: call it under torch.no_grad(), "
+                     "or give it detached tensors")
+
+
 def _bad_container(name: str, t):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a 1-D contiguous uint8 tensor")
@@ -710,7 +715,9 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     """x W^T + s_a (x A_a^T) B_a^T (fp32, M x N), a = adapter[m] (int32, -1 for
     none), with W (N x K bf16) given as a Split12 container on the device
     (wc12_linear_adapters): x M x K bf16, a L x r x K and b L x N x r bf16,
-    scales L fp32.  The plan serves batches of more than 16 tokens."""
+    scales L fp32.  The plan serves batches of more than 16 tokens.  For
+    serving: there is no gradient, and where one is asked for the call is
+    refused."""
     if not isinstance(cont, _Tensor) or cont.dtype is not _U8 or cont.dim() != 1 or not cont.is_cuda or not cont.is_contiguous():
         _bad_container("cont", cont)
     dev = cont.device
@@ -726,6 +733,8 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     a = _want("a", a, _BF16, (L, r, K), dev)
     b = _want("b", b, _BF16, (L, N, r), dev)
     scales = _want("scales", scales, _F32, (L,), dev)
+    if (x.requires_grad or a.requires_grad or b.requires_grad or scales.requires_grad) and torch.is_grad_enabled():
+        _no_gradient("split12_linear_adapters")
     plan_ptr, plan_bytes = None, 0
     if plan is not None:
         if not isinstance(plan, _Tensor) or plan.dtype is not _U8 or plan.dim() != 1 or plan.device != dev or not plan.is_contiguous():
@@ -753,7 +762,9 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
     the router's logits (T x E fp32) on, with the experts' weights given as
     two Split12 containers on the device, gate_up E x 2F x H and down
     E x H x F (wc12_moe): the k experts with the largest logits, their softmax
-    (over themselves, or without renormalize over all experts), SiLU-gated."""
+    (over themselves, or without renormalize over all experts), SiLU-gated.
+    For serving: there is no gradient, and where one is asked for the call is
+    refused."""
     if not isinstance(gate_up, _Tensor) or gate_up.dtype is not _U8 or gate_up.dim() != 1 or not gate_up.is_cuda or \
             not gate_up.is_contiguous():
         _bad_container("gate_up", gate_up)
@@ -769,6 +780,8 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
     T = x.shape[0]
     x = _want("x", x, _BF16, (T, H), dev)
     logits = _want("logits", logits, _F32, (T, E), dev)
+    if (x.requires_grad or logits.requires_grad) and torch.is_grad_enabled():
+        _no_gradient("split12_moe")
     if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("the output is bf16 or fp32")
     lib = _lib or load()
