@@ -715,9 +715,9 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     """x W^T + s_a (x A_a^T) B_a^T (fp32, M x N), a = adapter[m] (int32, -1 for
     none), with W (N x K bf16) given as a Split12 container on the device
     (wc12_linear_adapters): x M x K bf16, a L x r x K and b L x N x r bf16,
-    scales L fp32.  The plan serves batches of more than 16 tokens.  For
-    serving: there is no gradient, and where one is asked for the call is
-    refused."""
+    scales L fp32.  The plan serves batches of more than 16 tokens; a batch
+    of none does nothing.  For serving: there is no gradient, and where one is
+    asked for the call is refused."""
     if not isinstance(cont, _Tensor) or cont.dtype is not _U8 or cont.dim() != 1 or not cont.is_cuda or not cont.is_contiguous():
         _bad_container("cont", cont)
     dev = cont.device
@@ -743,6 +743,8 @@ def split12_linear_adapters(cont: torch.Tensor, N: int, K: int, x: torch.Tensor,
     lib = _lib or load()
     y = cont.new_empty((M, N), dtype=_F32) if out is None else _output(out, (M, N), _F32, dev)
     st = _status_word(status, dev)
+    if M == 0:  # the C call wants a token
+        return y
     work_bytes = lib.wc12_linear_adapters_work_bytes(M, r)
     work = cont.new_empty(work_bytes)
     rc = lib.wc12_linear_adapters(cont.data_ptr(), cont.numel(), plan_ptr, plan_bytes, N, K, x.data_ptr(), M, adapter.data_ptr(),

@@ -193,7 +193,7 @@ WC_API int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uint32_
  *                 aligned, for this call alone until it is done
  *   d_status      as for wc12_linear; WC_ERR_INVALID_ARG for an adapter
  *                 outside [-1, L), whose token gets the shared product only
- * K at most 65536, N below 2^22.  Up to 16 tokens the result is the same bits
+ * M >= 1, K at most 65536, N below 2^22.  Up to 16 tokens the result is the same bits
  * every time; beyond, as for wc12_linear, sums of parts of K are added in any order.
  * Two launches up to 16 tokens, then three and more (a token slice each).
  * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY (work_bytes too small)
