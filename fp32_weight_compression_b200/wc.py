@@ -695,6 +695,8 @@ def split12_embed(cont: torch.Tensor, V: int, K: int, ids: torch.Tensor, scale: 
         _bad("ids", ids, torch.int32 if isinstance(ids, _Tensor) and ids.dtype == torch.int32 else torch.int64, None, dev)
     if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("the output is bf16 or fp32")
+    if not 0 < V < 1 << 64 or not 0 < K < 1 << 32:  # what the C call's types hold
+        raise WCError(ERR_INVALID_ARG, "wc12_embed")
     if not ids.is_contiguous():
         ids = ids.contiguous()
     y = cont.new_empty((*ids.shape, K), dtype=dtype) if out is None else _output(out, (*ids.shape, K), dtype, dev)
@@ -786,6 +788,8 @@ def split12_moe(gate_up: torch.Tensor, down: torch.Tensor, E: int, H: int, F: in
         _no_gradient("split12_moe")
     if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("the output is bf16 or fp32")
+    if not 0 < k <= E or not 0 < F < 1 << 32:  # before a workspace is made by them
+        raise WCError(ERR_INVALID_ARG, "wc12_moe")
     lib = _lib or load()
     y = gate_up.new_empty((T, H), dtype=dtype) if out is None else _output(out, (T, H), dtype, dev)
     st = _status_word(status, dev)
