@@ -45,6 +45,21 @@ constexpr uint32_t kMaxExperts = 512;
 
 constexpr uint32_t kMaxPairs = kMaxTokens * kMaxTop;
 
+// How many stages' exceptions go into the lanes' queues at once, 64 values of a
+// lane in each: about 4 of the 16 that a queue holds, by the container's own
+// share of them, so that a warp hardly ever has to look its values up (see
+// stage_product_slow).  With one filling for a whole row that began at 16,384
+// values of H with an exception in 2,500 (8 tokens, 2 experts, 16384 x 8192: 2433
+// us, 399 so; 32768 x 4096: 4914 and 547), and in one of 4096 with one in 200
+// (5 tokens, 2 of 8, 4096 x 896: 246 us, 82 so; one in 100: 458 and 145).  The
+// rows that the shallow ring is for are not cut: the loop over their parts cost
+// its registers' spilling (16 tokens, 1024 x 1408: 63.6 -> 65.5 us).
+constexpr uint32_t kFill = 128;
+__device__ __forceinline__ uint32_t fill_stages(const View &v) {
+  const float room = float(v.n) / (16.0f * float(v.ne));  // an infinity without exceptions
+  return room < 2.0f ? 2u : room < float(kFill) ? uint32_t(room) : kFill;
+}
+
 // The (token, expert) pairs by expert, and the items: an expert and up to 8 of
 // its pairs; experts ascending.
 struct Route {
@@ -292,28 +307,36 @@ __global__ void __launch_bounds__(kThreads, kDepth == 3 ? 4 : 3) k12_moe_up(cons
   const XAt xat = x_rows(lane);
   const uint32_t g = lane >> 2, t = lane & 3;
   bool alive = true;
+  const uint32_t fill = fill_stages(v);
+  constexpr bool kParts = kDepth > 3;
   for (uint32_t job = first; job < jobs; job += clusters) {
-    exceptions_reset(x, lane);
-    if (v.ne > 0) {
-#pragma unroll 1
-      for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u0, u1, 2, i, lane, p.status);
-      exceptions_ready(x, u0, u1, lane);
-    }
-    now[0] = next[0];
-    now[1] = next[1];
-    entries(now, job + clusters);
-    offsets(next, job + 2 * clusters);
     float gate[1][4] = {}, up[1][4] = {};
-    for (uint32_t u = u0; alive && u < u1; u++, turn.next()) {
-      const uint32_t most = exceptions_most(x, 2 * u);
-      alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
-      if (!alive) break;
-      const uint32_t slot = ring + turn.slot * Up<kDepth>::kStage, xs = slot + 2 * kSubBytes;
-      const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
-      stage<1, 1, true, false>(gate, up, at, xat, v, x, most, K, lane, p.status);
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
-    }
+    uint32_t u = u0;
+    do {
+      const uint32_t end = kParts && u1 - u > fill ? u + fill : u1;
+      exceptions_reset(x, lane);
+      if (v.ne > 0) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < 2; i++) window_keep(x, i ? now[1] : now[0], v, row_of(job, i), K, u, end, 2, i, lane, p.status);
+        exceptions_ready(x, u, end, lane);
+      }
+      if (end == u1) {
+        now[0] = next[0];
+        now[1] = next[1];
+        entries(now, job + clusters);
+        offsets(next, job + 2 * clusters);
+      }
+      for (; alive && u < end; u++, turn.next()) {
+        const uint32_t most = exceptions_most(x, 2 * u);
+        alive = bar_wait(bars, &bars.full[turn.slot], turn.parity, true, p.status);
+        if (!alive) break;
+        const uint32_t slot = ring + turn.slot * Up<kDepth>::kStage, xs = slot + 2 * kSubBytes;
+        const StageAt at{slot, warp, xs, xs, 0, false, 2 * u, u, u, row_of(job, 0), row_of(job, 1)};
+        stage<1, 1, true, false>(gate, up, at, xat, v, x, most, K, lane, p.status);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.empty[turn.slot]);
+      }
+    } while (kParts && alive && u < u1);
     const uint32_t item = job / tiles, n = r.item_n[item], from = r.item_first[item], f0 = (job - item * tiles) * kSubRows;
     if (csize == 1) {  // a lane has both sums of its rows and columns
 #pragma unroll
@@ -448,10 +471,11 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
     x.q = reinterpret_cast<Queues *>(dyn + Down::kQueues + warp * sizeof(Queues));
     const XAt xat = x_rows(lane);
     const bool wild = book_wild(v.book);
+    const uint32_t fill = fill_stages(v);
     uint32_t st = st0;
     bool alive = true;
-    for (uint32_t q = q0, item = first; alive && q < q1; item++, st = 0) {
-      const uint32_t end = q1 - q < per - st ? st + (q1 - q) : per;
+    for (uint32_t q = q0, item = first; alive && q < q1;) {
+      const uint32_t last_st = q1 - q < per - st ? st + (q1 - q) : per, end = last_st - st > fill ? st + fill : last_st;
       exceptions_reset(x, lane);
       if (v.ne > 0) {
         const bool some = window_keep(x, now, v, row_of(item), K, 2 * st, 2 * end, 1, 0, lane, p.status);
@@ -459,9 +483,11 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
         x.short_of = x.short_of || __any_sync(0xffffffffu, some);
       }
       x.short_of = x.short_of || wild;
-      now = next;
-      entries(now, item + 1);
-      offsets(next, item + 2);
+      if (end == last_st) {
+        now = next;
+        entries(now, item + 1);
+        offsets(next, item + 2);
+      }
       float tot0[1][4] = {}, tot1[1][4] = {};
       for (; st < end; st++, q++, turn.next()) {
         const uint32_t most = exceptions_most(x, 2 * st);
@@ -483,6 +509,10 @@ __global__ void __launch_bounds__(kThreads, 3) k12_moe_down(const __grid_constan
           to[0] += tot0[0][i] + tot1[0][i];
           to[8] += tot0[0][2 + i] + tot1[0][2 + i];
         }
+      if (st == per) {
+        item++;
+        st = 0;
+      }
     }
   }
   if (csize > 1) cluster_sync(); else __syncthreads();

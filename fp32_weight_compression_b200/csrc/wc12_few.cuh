@@ -731,7 +731,8 @@ __device__ __forceinline__ void stage_product(float tot0[kTiles][4], float tot1[
 // 8 tokens, an exception in 200 values: 227 -> 67 us, one in 100: 412 -> 99).
 // The experts' kernels do without: the compiler keeps more of their loops'
 // values elsewhere with it (5 tokens, large experts 53.4 -> 56.3 us, 16 tokens
-// 63 -> 68).
+// 63 -> 68).  They fill the queues for a part of a row at a time instead, outside
+// the loop over the part's stages.
 // Weights that are not finite meet a value's first part only: times a second
 // part, which is zero or of the other sign as often as not, an infinite one
 // would turn the sum into NaN.
