@@ -227,9 +227,11 @@ WC_API int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const voi
  *   d_status      device i32 set to 0 by the caller: WC_ERR_CORRUPT for a bad
  *                 container
  * A token whose logits are all -inf gets zeros; one with a NaN or +inf among
- * them a row of NaN.  A token's row does not depend on the other tokens'
- * values.  Three launches for each 32 tokens; the same bits every time.  T = 0
- * does nothing.  Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
+ * them a row of NaN.  Other tokens' values, infinities and NaN among them, never
+ * reach a token's row, but its rounding depends on the batch: the experts that
+ * the others choose move the places where a sum over experts is parted.  Three
+ * launches for each 32 tokens; the same call gives the same bits every time.
+ * T = 0 does nothing.  Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
  * (work_bytes too small) or WC_ERR_CUDA. */
 WC_API uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F);
 WC_API int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const void *d_down,
