@@ -10,16 +10,17 @@
 //   * few tokens (kFewTokens): one kernel streams W through registers
 //     (wc12_few.cuh), waits for t only when its sums are done, and adds t B^T
 //     to them.  The kernel that makes t runs beside it (programmatic dependent
-//     launch).  4096 x 4096, 1 token: 10.3 us (25 MB, from L2); 4096 x 14336,
-//     7 tokens: 25.3 (90 MB); 14336 x 4096, 16 tokens: 33 (99 MB), where the tensor-
-//     memory kernel takes 36.5 for the shared product alone;
+//     launch).  Graph replays: 4096 x 4096, 1 token: 10.3 us (25 MB, from L2);
+//     4096 x 14336, 7 tokens: 25.3 (90 MB); 14336 x 4096, 16 tokens: 32.5 (99 MB),
+//     where the tensor-memory kernel takes 36.5 for the shared product alone;
 //   * more: Y starts as the adapters' part, from a tensor-core product of t
 //     (as the sum of three bf16 numbers) and B, and the tensor-memory kernel
 //     of k_split12_linear.cu, which starts beside that and needs Y at its end
-//     only, adds the shared product to it.  4096 x 4096, 203 tokens, rank 64:
-//     37 us (41 one after another); 14336 x 4096, 2048 tokens: 505, of which
-//     the shared product's eight slices take 475: each brings all tokens to
-//     each block of rows again, and twice as many a slice took twice as long.
+//     only, adds the shared product to it.  Graph replays: 4096 x 4096, 203
+//     tokens, rank 64: 36.5 us (41 one after another); 14336 x 4096, 2048 tokens:
+//     503 to 514, of which the shared product's eight slices take 475: each brings
+//     all tokens to each block of rows again, and twice as many a slice took
+//     twice as long.
 #include <cstdint>
 
 #include "wc12_few.cuh"

@@ -8,9 +8,10 @@
 // each 65,536-value chunk that it touches (usually one): their offsets are
 // read beside the row's bytes, the list's entries before the row is written,
 // and the exceptions' values go over it after a barrier.  A long list is
-// narrowed down first.  Latency bounds few rows (id, row, write: three round
-// trips; 2.3 us for 1 or 61 rows of 1024, of which the launch is most), the
-// memory's rate many: 8192 rows of 4096, 118 MB, in 23 us, 5.1 TB/s (36 us
+// narrowed down first.  Times of graph replays: latency bounds few rows (id,
+// row, write: three round trips; 2.3 us for 1 or 61 rows of 1024, of which the
+// launch is most), issue and memory many: 8192 rows of 4096, 118 MB, in 23 us,
+// 5.1 TB/s, with 76 % of the issue slots taken (36 us
 // with one piece of a row in flight and the exceptions read after it; 34 with
 // two pieces; six CTAs an SM, 25.5 without the bound on registers).
 #include <cstdint>

@@ -19,10 +19,11 @@
 //     D_e of every item as through one long row, whose parts its CTAs take.
 //     The weighted sum over experts is part of the product's sum: no atomics,
 //     one rounding, one write.
-// Times: 1 token, 8 of 64 experts of 2048 x 768: 28 us (57 MB); 5 tokens, 2 of
-// 8, 4096 x 1792: 54 (200 MB); 16 tokens, 4 of 32, 1024 x 1408: 63 (180 MB); 32
-// tokens, 8 of 128, 2048 x 768: 200 (790 MB, 3.9 TB/s; the up product alone
-// reads 631 MB in 113 us, 5.6 TB/s).
+// Times of graph replays: 1 token, 8 of 64 experts of 2048 x 768: 29 us (57 MB);
+// 5 tokens, 2 of 8, 4096 x 1792: 55 (200 MB); 16 tokens, 4 of 32, 1024 x 1408: 63
+// (180 MB); 32 tokens, 8 of 128, 2048 x 768: 206 (790 MB, 3.8 TB/s).  In the last
+// the up product alone takes 110 us for 524 MB of weights, 4.8 TB/s; from DRAM
+// come 609 MB, some of it twice.
 //
 // k12_moe_route finds the experts first, a warp a token.  The up product starts
 // when that is done; the down product starts beside the up product (programmatic
@@ -52,8 +53,10 @@ constexpr uint32_t kMaxPairs = kMaxTokens * kMaxTop;
 // values of H with an exception in 2,500 (8 tokens, 2 experts, 16384 x 8192: 2433
 // us, 399 so; 32768 x 4096: 4914 and 547), and in one of 4096 with one in 200
 // (5 tokens, 2 of 8, 4096 x 896: 246 us, 82 so; one in 100: 458 and 145).  The
-// rows that the shallow ring is for are not cut: the loop over their parts cost
-// its registers' spilling (16 tokens, 1024 x 1408: 63.6 -> 65.5 us).
+// rows that the shallow ring is for are not cut, though they come to looking up
+// at one in 200 (16 tokens, 4 of 32, 1024 x 1408: 298 us for 54): the loop over
+// their parts made its kernel spill registers, at every share of exceptions (63.5
+// -> 67.7 us on that shape's listed case).
 constexpr uint32_t kFill = 128;
 __device__ __forceinline__ uint32_t fill_stages(const View &v) {
   const float room = float(v.n) / (16.0f * float(v.ne));  // an infinity without exceptions
@@ -577,8 +580,9 @@ extern "C" int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const
   if (!aligned(d_x, 16) || !aligned(d_logits, 4) || !aligned(d_out, 4) || !aligned(d_work, 16)) return WC_ERR_INVALID_ARG;
   if (work_bytes < wc12_moe_work_bytes(T, k, F)) return WC_ERR_CAPACITY;
   // rows of H that are long enough fill a deeper ring of fewer CTAs (32 tokens,
-  // 128 experts, H 2048: 200 us with 4 stages, 216 with 3); of shorter ones
-  // more CTAs run, whose ends overlap (16 tokens, H 1024: 64 us against 76)
+  // 128 experts, H 2048: 200 us with 4 stages, 216 with 3, both before the up
+  // product became an ordinary launch); of shorter ones more CTAs run, whose
+  // ends overlap (16 tokens, H 1024: 64 us against 76)
   const bool deep = H >= 2048;
   const int slots = deep ? up_slots<4>() : up_slots<3>(), sms = slots > 0 ? wc12l::device_sms() : 0;
   if (sms <= 0) return cuda_failed();

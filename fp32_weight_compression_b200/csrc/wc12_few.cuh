@@ -27,8 +27,9 @@
 // What bounds it: the expansion's instructions (see high8) and, in short rows,
 // what comes before the first stage and after the last (header, exceptions,
 // joining the parts of K: 4 to 6 us), not the memory.  14336 x 4096, 16
-// tokens, adapters of rank 16 (98.6 MB): 33 us, 3.0 TB/s, where the boxes
-// alone stream in 17, and the kernel without products and exceptions takes 23.  Ways that were left: loads into registers (57 us: the
+// tokens, adapters of rank 16 (98.6 MB), replayed from a graph: 32.5 us, 3.0
+// TB/s, where the boxes alone stream in 17, and the kernel without products and
+// exceptions takes 23.  Ways that were left: loads into registers (57 us: the
 // tokens' values came from L2 at the moment of use); copies by cp.async, a
 // lane its own pieces (56: twice the product's instructions); eight warps a
 // CTA with a subtile each (64: half the independent products a lane has,
@@ -46,8 +47,9 @@
 // in flight (or the ones of the rows before), and gives those of its part of
 // K to the lanes that will hold their values, each of which has a short
 // queue.  The products take a lane's next entry in passing, without a branch.
-// More than a queue holds: the queues are filled again on the way, or each lane's
-// values are looked up in the container's sorted lists (see stage_product_slow).
+// More than a queue holds: the queues are filled again on the way, or for a part
+// of the row at a time, or each lane's values are looked up in the container's
+// sorted lists (see stage_product_slow).
 #pragma once
 
 #include <cstdint>

@@ -194,7 +194,10 @@ WC_API int32_t wc12_embed(const void *d_w, uint64_t w_bytes, uint64_t V, uint32_
  *   d_status      as for wc12_linear; WC_ERR_INVALID_ARG for an adapter
  *                 outside [-1, L), whose token gets the shared product only
  * M >= 1, K at most 65536, N below 2^22.  Up to 16 tokens the result is the same bits
- * every time; beyond, as for wc12_linear, sums of parts of K are added in any order.
+ * every time; beyond, as for wc12_linear, sums of parts of K are added in any
+ * order, and tensor memory, whose sums are cut off rather than rounded, holds
+ * them (14336 x 4096, 2048 tokens: off by 2.2e-6 of the output's norm, up to 16
+ * tokens by 1.1e-7).  Infinities and NaN come out where the formula has them.
  * Two launches up to 16 tokens, then three and more (a token slice each).
  * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY (work_bytes too small)
  * or WC_ERR_CUDA. */
@@ -231,7 +234,10 @@ WC_API int32_t wc12_linear_adapters(const void *d_w, uint64_t w_bytes, const voi
  * reach a token's row, but its rounding depends on the batch: the experts that
  * the others choose move the places where a sum over experts is parted.  Three
  * launches for each 32 tokens; the same call gives the same bits every time.
- * T = 0 does nothing.  Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
+ * T = 0 does nothing.  Meant for up to two exceptions in 1,000 of the
+ * containers' values (serving weights have one in 2,500 and fewer): at one in 100
+ * the call takes five times as long, where H is below 2048 ten times and more.
+ * Returns WC_OK, WC_ERR_INVALID_ARG, WC_ERR_CAPACITY
  * (work_bytes too small) or WC_ERR_CUDA. */
 WC_API uint64_t wc12_moe_work_bytes(uint32_t T, uint32_t k, uint32_t F);
 WC_API int32_t wc12_moe(const void *d_gate_up, uint64_t gate_up_bytes, const void *d_down,
